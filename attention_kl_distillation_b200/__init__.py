@@ -14,10 +14,15 @@ _BINDING_NAMES = ("StreamKLError", "bwd", "bwd_algorithm_for", "bwd_noalloc", "f
                   "launch_count", "query_device_status", "set_bwd_algorithm", "set_wait_limit_ms",
                   "splitk_suggest", "splitk_workspace_size", "streamkl", "workspace_size")
 
-__all__ = list(_BINDING_NAMES)
+_DIFF_NAMES = ("attn_paged", "diff_attn", "diff_attn_bwd", "diff_attn_fwd", "diff_attn_paged",
+               "diff_attn_workspace_size", "paged_workspace_size", "paged_write")
+
+__all__ = [*_BINDING_NAMES, *_DIFF_NAMES]
 
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
         return getattr(importlib.import_module(".binding", __name__), name)
+    if name in _DIFF_NAMES:
+        return getattr(importlib.import_module(".diff", __name__), name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,765 @@
+// diff_bwd_sm100.cu -- backward of differential attention for sm_100a.
+//
+// With G = dO V^T, P_t = 2^(c_t x_t - LSE_t log2e) regenerated from the saved
+// LSEs and D_t[i] = <dO[i], O_t[i]>,
+//
+//   A   = P1 - lam P2              dV   = A^T dO
+//   X1  = P1 (G - D1)              dQ1  = s1 X1 K1    dK1 = s1 X1^T Q1
+//   X2  = lam P2 (D2 - G)          dQ2  = s2 X2 K2    dK2 = s2 X2^T Q2
+//   dlam[i] = -D2[i], summed over what lam is broadcast over
+//
+// Two passes of one kernel template, each with a resident 128-row tile R and
+// streamed 64-row tiles C, so that every gradient is accumulated in TMEM by one
+// CTA in a fixed order: no atomics, and results that repeat bit for bit.
+//
+//   kDiffKV  R = K1, K2, V   C = Q1, Q2, dO of every query head that shares
+//            the key head: its gradients are one sum over the group
+//   kDiffQ   R = Q1, Q2, dO  C = K1, K2, V
+//
+// Per step: S1, S2 and G (M = 128 resident rows, N = 64 streamed rows) by
+// tcgen05 from shared memory; the compute warps turn them into X1, X2 and A in
+// 16 bits and store those to TMEM, where they are the A operands of the output
+// products OUT += X C (C read with its features contiguous).
+// TMEM: S1 [0,64) S2 [64,128) G [128,192) X1 [192,224) X2 [224,256) OUT [256,..)
+// A replaces G (each 16-column group by the warpgroup that read it).
+//
+// S of step t+1 is issued as soon as the warps have read S of step t, so it and
+// the exponentials overlap; G of step t+1 is queued behind the products of step
+// t, and its commit therefore also says that X1, X2 and A may be overwritten.
+//
+// TMEM holds 256 output columns beside the 256 above, shared memory the
+// resident tiles and two stages. That decides the passes:
+//   d = 64            kDiffKV gives dK1, dK2 and dV at once
+//   d = 128           dV has a pass of its own (S1, S2 only; 128 value columns)
+//   d = 128, dv = 256 kDiffKV and kDiffQ take one map per launch (SEL 1, 2):
+//                     V, dO and both maps' tiles do not fit at once
+//
+// What bounds it: the issue of M128 N64 products, about 64 clocks each whatever
+// their N up to 128, beside 4 exponentials per visible pair over both passes.
+#include "diff_sm100.cuh"
+
+#include <type_traits>
+
+namespace skl {
+namespace {
+
+constexpr int R = kDiffRows;
+constexpr int CB = kDiffStep;
+constexpr int NWG = 4;             // compute warpgroups
+constexpr int CPW = CB / NWG;      // streamed rows per compute warpgroup
+constexpr int NTHREADS = (3 + 1 + 4 * NWG) * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kColS2 = 64, kColG = 128, kColX1 = 192, kColX2 = 224, kColOut = 256;
+constexpr int kNever = 1 << 30;
+
+template <int PASS, int D, int DV, int SEL>
+struct BwdLay {
+  static constexpr bool KV = PASS == kDiffKV;
+  static constexpr bool S1 = (SEL & 5) != 0, S2 = (SEL & 6) != 0;  // maps whose P is formed
+  static constexpr bool X1 = (SEL & 1) != 0, X2 = (SEL & 2) != 0;
+  static constexpr bool WG = (SEL & 3) != 0, WV = (SEL & 4) != 0;
+  static constexpr int r1 = S1 ? R * D * 2 : 0;
+  static constexpr int r2 = S2 ? R * D * 2 : 0;
+  static constexpr int r3 = WG ? R * DV * 2 : 0;   // the dV-only pass needs no V
+  static constexpr int c1 = S1 ? CB * D * 2 : 0;
+  static constexpr int c2 = S2 ? CB * D * 2 : 0;
+  static constexpr int c3 = CB * DV * 2;
+  static constexpr int rec = KV ? CB * kDiffRec * 4 : 0;
+  static constexpr int load_bytes = c1 + c2 + c3 + rec;
+  static constexpr int stage = c1 + c2 + c3 + (rec ? 2048 : 0);
+  static constexpr int c_off = r1 + r2 + r3;
+  static constexpr int fit = (232448 - 1024 - 512 - c_off) / stage;
+  static constexpr int NST = fit > 4 ? 4 : fit;
+  static constexpr int bar_off = c_off + NST * stage;
+  // cfull[NST] cempty[NST] craw[NST] rfull rempty sfull sempty gfull xfull ofull oempty drain
+  static constexpr int nbar = 3 * NST + 9;
+  static constexpr int misc_off = bar_off + nbar * 8;
+  static constexpr int alloc = misc_off + 16 + 1024;
+  static constexpr int o1 = kColOut;
+  static constexpr int o2 = o1 + (X1 ? D : 0);
+  static constexpr int o3 = o2 + (X2 ? D : 0);
+  static_assert(o3 + (WV ? DV : 0) <= 512, "TMEM budget exceeded");
+  static_assert(NST >= 2, "streamed ring too shallow");
+  static_assert(alloc <= 232448, "shared memory budget exceeded");
+  static_assert(!(PASS == kDiffQ && WV), "dV belongs to the key pass");
+};
+
+// A unit: 128 resident rows, and the streamed tiles [c_first, c_first + tiles)
+// of each of `heads` query heads (kQ: of one key head).
+struct BwdUnit {
+  int b, h, hk, half, r0, c_first, tiles, heads, lo, hi;
+  Lens l;
+  // Streamed rows [lo, hi) are in the problem; a tile that reaches past either
+  // end, yet not beyond the tensor, is ragged and cleaned before use.
+  __device__ __forceinline__ bool ragged(int tile, int n) const {
+    const int c0 = (c_first + tile) * CB;
+    return c0 < lo || (c0 + CB > hi && hi < n);
+  }
+};
+
+template <int PASS>
+__device__ __forceinline__ BwdUnit decode(const DiffBwdParams& p, int u) {
+  BwdUnit w;
+  const int off_first = 0;
+  w.half = u % p.nhalf;
+  u /= p.nhalf;
+  if (PASS == kDiffKV) {
+    // key tiles that the most rows see first, heads innermost
+    const int BH = p.s.B * p.s.HK;
+    const int bh = u % BH;
+    w.r0 = (u / BH) * R;
+    w.b = bh / p.s.HK;
+    w.hk = bh % p.s.HK;
+    w.heads = p.s.H / p.s.HK;
+    w.h = w.hk * w.heads;
+    w.l = diff_lens(p.s, w.b);
+    const int off = w.l.k - w.l.q;
+    w.lo = p.s.causal ? max(0, -off) : 0;  // rows before see no key at all
+    w.hi = w.l.q;
+    int first = w.lo;
+    if (p.s.causal) first = max(first, w.r0 - off);  // first row that sees key r0
+    w.c_first = first / CB;
+    w.tiles = (w.r0 < w.l.k && first < w.hi) ? (w.hi + CB - 1) / CB - w.c_first : 0;
+  } else {
+    const int BH = p.s.B * p.s.H;
+    const int nrt = (p.s.NQ + R - 1) / R;
+    const int bh = u % BH;
+    w.r0 = (nrt - 1 - u / BH) * R;
+    w.b = bh / p.s.H;
+    w.h = bh % p.s.H;
+    w.hk = w.h / (p.s.H / p.s.HK);
+    w.heads = 1;
+    w.l = diff_lens(p.s, w.b);
+    w.lo = 0;
+    w.hi = w.l.k;
+    int keys = w.l.k;
+    if (p.s.causal) keys = min(keys, min(w.r0 + R, w.l.q) + w.l.k - w.l.q);
+    if (w.r0 >= w.l.q) keys = 0;
+    w.c_first = off_first;
+    w.tiles = keys > 0 ? (keys + CB - 1) / CB : 0;
+  }
+  return w;
+}
+
+// X1, X2 and A of one resident row and CPW streamed rows.  Per streamed row
+// (KV) or for the thread's own row: rec = -LSE1 log2e, -LSE2 log2e, D1, D2, lam.
+// Streamed rows i in [lo, hi] are visible (MASK only).
+template <class Lay, bool MASK, bool F16>
+__device__ __forceinline__ void form_p(uint32_t (&s1)[CPW], uint32_t (&s2)[CPW], const float* rr,
+                                       const float (&rec)[kDiffRec], float c1, float c2, int lo,
+                                       int hi) {
+  // P1 over s1 and lam P2 over s2
+  const float2 C1 = make_float2(c1, c1), C2 = make_float2(c2, c2);
+#pragma unroll
+  for (int q = 0; q < CPW; q += 4) {
+    float4 b1 = make_float4(rec[0], rec[0], rec[0], rec[0]);
+    float4 b2 = make_float4(rec[1], rec[1], rec[1], rec[1]);
+    float4 lm = make_float4(rec[4], rec[4], rec[4], rec[4]);
+    if (Lay::KV) {
+      if (Lay::S1) b1 = ld_shared_f4(rr + 0 * CB + q);
+      if (Lay::S2) b2 = ld_shared_f4(rr + 1 * CB + q);
+      if (Lay::S2) lm = ld_shared_f4(rr + 4 * CB + q);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = q + 2 * e;
+      const bool vx = !MASK || (i >= lo && i <= hi), vy = !MASK || (i + 1 >= lo && i + 1 <= hi);
+      if (Lay::S1) {
+        const float2 x = make_float2(__uint_as_float(s1[i]), __uint_as_float(s1[i + 1]));
+        const float2 u = __ffma2_rn(x, C1, e ? make_float2(b1.z, b1.w) : make_float2(b1.x, b1.y));
+        s1[i] = vx ? __float_as_uint(ex2(u.x)) : 0u;
+        s1[i + 1] = vy ? __float_as_uint(ex2(u.y)) : 0u;
+      }
+      if (Lay::S2) {
+        const float2 x = make_float2(__uint_as_float(s2[i]), __uint_as_float(s2[i + 1]));
+        const float2 u = __ffma2_rn(x, C2, e ? make_float2(b2.z, b2.w) : make_float2(b2.x, b2.y));
+        const float2 r = __fmul2_rn(make_float2(vx ? ex2(u.x) : 0.f, vy ? ex2(u.y) : 0.f),
+                                    e ? make_float2(lm.z, lm.w) : make_float2(lm.x, lm.y));
+        s2[i] = __float_as_uint(r.x);
+        s2[i + 1] = __float_as_uint(r.y);
+      }
+    }
+  }
+}
+
+template <int PASS, int D, int DV, int SEL, bool F16>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    streamkl_diff_bwd_kernel(const __grid_constant__ DiffBwdParams p) {
+  using Lay = BwdLay<PASS, D, DV, SEL>;
+  constexpr int NST = Lay::NST;
+  constexpr bool KV = Lay::KV;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* cfull = reinterpret_cast<uint64_t*>(smem + Lay::bar_off);
+  uint64_t* cempty = cfull + NST;
+  uint64_t* craw = cempty + NST;  // a ragged tile has landed, to be cleaned
+  uint64_t* rfull = craw + NST;
+  uint64_t* rempty = rfull + 1;
+  uint64_t* sfull = rempty + 1;  // S1, S2 of a step are in TMEM
+  uint64_t* sempty = sfull + 1;  // ... and have been read
+  uint64_t* gfull = sempty + 1;  // G is in TMEM, and the products of the step before are done
+  uint64_t* xfull = gfull + 1;   // X1, X2, A are in TMEM
+  uint64_t* ofull = xfull + 1;
+  uint64_t* oempty = ofull + 1;
+  uint64_t* drain = oempty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::misc_off);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::misc_off + 4);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns};
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&cfull[s], 1);
+      mbar_init(&cempty[s], 1);
+      mbar_init(&craw[s], 1);
+    }
+    mbar_init(rfull, 1);
+    mbar_init(rempty, 1);
+    mbar_init(sfull, 1);
+    mbar_init(sempty, 4 * NWG);
+    mbar_init(gfull, 1);
+    mbar_init(xfull, 4 * NWG);
+    mbar_init(ofull, 1);
+    mbar_init(oempty, 4 * NWG);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    if (Lay::S1) tma_prefetch_desc(&p.tmR1);
+    if (Lay::S2) tma_prefetch_desc(&p.tmR2);
+    if (Lay::WG) tma_prefetch_desc(&p.tmR3);
+    if (Lay::S1) tma_prefetch_desc(&p.tmC1);
+    if (Lay::S2) tma_prefetch_desc(&p.tmC2);
+    tma_prefetch_desc(&p.tmC3);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  uint8_t* r1_s = smem;
+  uint8_t* r2_s = r1_s + Lay::r1;
+  uint8_t* r3_s = r2_s + Lay::r2;
+  auto c1_s = [&](int s) { return smem + Lay::c_off + s * Lay::stage; };
+  auto c2_s = [&](int s) { return c1_s(s) + Lay::c1; };
+  auto c3_s = [&](int s) { return c1_s(s) + Lay::c1 + Lay::c2; };
+  auto rec_s = [&](int s) { return reinterpret_cast<float*>(c1_s(s) + Lay::c1 + Lay::c2 + Lay::c3); };
+  const int nrows = KV ? p.s.NK : p.s.NQ;    // resident extent
+  const int nstream = KV ? p.s.NQ : p.s.NK;  // streamed extent
+  SnakeSched sched(p.s.B * (KV ? p.s.HK : p.s.H) * ((nrows + R - 1) / R) * p.nhalf);
+  int u;
+
+  // Of the launch's 96 registers x 640 threads the first warpgroup hands over
+  // what it does not need (128 x 64 + 512 x 104 = 640 x 96).
+  if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // ------------------------------------------------------------ compute
+    const int part = (warp - 4) >> 2;  // streamed rows [part*CPW, part*CPW + CPW) of each step
+    const int quarter = warp & 3;
+    const int j = quarter * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    int cs = 0;
+    uint32_t cph = 0, sph = 0, gph = 0, oph = 0;
+    bool ok = true;
+    while (ok && sched.next(u)) {
+      const BwdUnit w = decode<PASS>(p, u);
+      const int row = w.r0 + j;  // key (kKV) or query (kQ)
+      const int off = w.l.k - w.l.q;
+      float rec[kDiffRec] = {-INFINITY, -INFINITY, 0.f, 0.f, 0.f};
+      if (!KV && row < w.l.q && w.tiles) {
+        const float* r = p.rec + (static_cast<size_t>(w.b * p.s.H + w.h) * p.NQpad + (row / CB) * CB) *
+                                     kDiffRec + (row % CB);
+#pragma unroll
+        for (int f = 0; f < kDiffRec; ++f) rec[f] = r[f * CB];
+      }
+      const int steps = w.heads * w.tiles;
+      int tile = 0;
+      for (int t = 0; t < steps; ++t) {
+        const int c0 = (w.c_first + tile) * CB;
+        const int cc = c0 + part * CPW;
+        if (++tile == w.tiles) tile = 0;
+        if (KV && !(ok = mbar_wait(&cfull[cs], cph, ctl))) break;  // the step's records
+        if (!(ok = mbar_wait(sfull, sph, ctl))) break;
+        sph ^= 1;
+        tc_fence_after();
+        uint32_t a[CPW], b[CPW], g[CPW];
+        if (Lay::S1) tmem_ld_32x32b_x16(tl + part * CPW, a);
+        if (Lay::S2) tmem_ld_32x32b_x16(tl + kColS2 + part * CPW, b);
+        tmem_ld_wait();
+        if (Lay::S1) reg_fence(a);
+        if (Lay::S2) reg_fence(b);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sempty);
+        // visible streamed rows lo..hi; rows that see nothing have P = 0 from their record
+        int lo = -kNever, hi = kNever;
+        bool masked;
+        if (KV) {
+          masked = p.s.causal && c0 + off < w.r0 + R - 1;
+          if (p.s.causal) lo = row - off - cc;
+        } else {
+          masked = c0 + CB > w.l.k || (p.s.causal && c0 + CB - 1 > w.r0 + off);
+          hi = w.l.k - 1 - cc;
+          if (p.s.causal) hi = min(hi, row + off - cc);
+        }
+        const float* rr = KV ? rec_s(cs) + part * CPW : nullptr;
+        if (masked)
+          form_p<Lay, true, F16>(a, b, rr, rec, p.c1, p.c2, lo, hi);
+        else
+          form_p<Lay, false, F16>(a, b, rr, rec, p.c1, p.c2, lo, hi);
+        if (!(ok = mbar_wait(gfull, gph, ctl))) break;
+        gph ^= 1;
+        tc_fence_after();
+        if (Lay::WG) {
+          tmem_ld_32x32b_x16(tl + kColG + part * CPW, g);
+          tmem_ld_wait();
+          reg_fence(g);
+        }
+        uint32_t w1[CPW / 2], w2[CPW / 2], w3[CPW / 2];
+#pragma unroll
+        for (int q = 0; q < CPW; q += 4) {
+          float4 d1 = make_float4(rec[2], rec[2], rec[2], rec[2]);
+          float4 d2 = make_float4(rec[3], rec[3], rec[3], rec[3]);
+          if (KV && Lay::X1) d1 = ld_shared_f4(rr + 2 * CB + q);
+          if (KV && Lay::X2) d2 = ld_shared_f4(rr + 3 * CB + q);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int i = q + 2 * e;
+            const float2 NEG = make_float2(-1.f, -1.f);
+            const float2 P1 = Lay::S1 ? make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])) : NEG;
+            const float2 P2 = Lay::S2 ? make_float2(__uint_as_float(b[i]), __uint_as_float(b[i + 1])) : NEG;
+            const float2 G = Lay::WG ? make_float2(__uint_as_float(g[i]), __uint_as_float(g[i + 1])) : NEG;
+            if (Lay::X1) {
+              const float2 d = e ? make_float2(d1.z, d1.w) : make_float2(d1.x, d1.y);
+              float2 x = __fmul2_rn(P1, __ffma2_rn(d, NEG, G));
+              w1[i / 2] = pack2<F16>(x.x, x.y);
+            }
+            if (Lay::X2) {
+              const float2 d = e ? make_float2(d2.z, d2.w) : make_float2(d2.x, d2.y);
+              float2 x = __fmul2_rn(P2, __ffma2_rn(G, NEG, d));
+              w2[i / 2] = pack2<F16>(x.x, x.y);
+            }
+            if (Lay::WV) {
+              const float2 x = __ffma2_rn(P2, NEG, P1);
+              w3[i / 2] = pack2<F16>(x.x, x.y);
+            }
+          }
+        }
+        if (Lay::X1) tmem_st_32x32b_x8(tl + kColX1 + part * (CPW / 2), w1);
+        if (Lay::X2) tmem_st_32x32b_x8(tl + kColX2 + part * (CPW / 2), w2);
+        if (Lay::WV)
+          tmem_st_32x32b_x8(tl + (Lay::WG ? kColG + part * CPW : kColX1 + part * (CPW / 2)), w3);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(xfull);
+        if (++cs == NST) {
+          cs = 0;
+          cph ^= 1;
+        }
+      }
+      if (!ok) break;
+      // Unit epilogue: this warpgroup writes a quarter of each output's columns.
+      if (steps > 0) {
+        if (!(ok = mbar_wait(ofull, oph, ctl))) break;
+        oph ^= 1;
+        tc_fence_after();
+      }
+      const bool in_tensor = row < nrows;
+      // rows behind their sequence, and rows that see nothing, get exact zeros
+      const bool live = steps > 0 && row < (KV ? w.l.k : w.l.q) &&
+                        (KV || !p.s.causal || row + off >= 0);
+      auto write = [&](void* dst, const Strides& st, uint32_t col, auto width_c, int first, float f) {
+        constexpr int W = decltype(width_c)::value / NWG;
+        const int h = KV ? w.hk : w.h;
+        uint16_t* o = static_cast<uint16_t*>(dst) + w.b * st.b + h * st.h + row * st.n + first + part * W;
+#pragma unroll
+        for (int c = 0; c < W; c += 16) {
+          uint32_t v[16];
+          if (steps > 0) {
+            tmem_ld_32x32b_x16(tl + col + part * W + c, v);
+            tmem_ld_wait();
+            reg_fence(v);
+          }
+          uint32_t x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            x[k] = live ? pack2<F16>(__uint_as_float(v[2 * k]) * f, __uint_as_float(v[2 * k + 1]) * f) : 0u;
+          if (in_tensor) {
+            *reinterpret_cast<uint4*>(o + c) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4*>(o + c + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+          }
+        }
+      };
+      using WD = std::integral_constant<int, D>;
+      using WDV = std::integral_constant<int, DV>;
+      if (Lay::X1 && p.out1) write(p.out1, p.so1, Lay::o1, WD{}, 0, p.s1);
+      if (Lay::X2 && p.out2) write(p.out2, p.so2, Lay::o2, WD{}, 0, p.s2);
+      if (Lay::WV && p.out3) write(p.out3, p.so3, Lay::o3, WDV{}, w.half * DV, 1.f);
+      if (steps > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(oempty);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      if (lane == 0) {
+        int cs = 0;
+        uint32_t rph = 0, cph = 0, rawph = 0;  // bit s of rawph: parity of craw[s]
+        uint32_t armed_r = 0, armed_c[NST] = {};  // last armed phase + 1; + 2 on craw
+        bool ok = true;
+        while (ok && sched.next(u)) {
+          const BwdUnit w = decode<PASS>(p, u);
+          if (w.tiles == 0) continue;
+          if (!(ok = mbar_wait(rempty, rph ^ 1, ctl))) break;
+          mbar_arrive_expect_tx(rfull, Lay::r1 + Lay::r2 + Lay::r3);
+          const int rh = KV ? w.hk : w.h;
+  #pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            if (Lay::S1) tma_load_4d(r1_s + c * (R * 128), &p.tmR1, rfull, c * 64, w.r0, rh, w.b);
+            if (Lay::S2) tma_load_4d(r2_s + c * (R * 128), &p.tmR2, rfull, c * 64, w.r0, rh, w.b);
+          }
+          if (Lay::WG) {
+            // V is read per key head, dO per query head
+  #pragma unroll
+            for (int c = 0; c < DV / 64; ++c)
+              tma_load_4d(r3_s + c * (R * 128), &p.tmR3, rfull, c * 64, w.r0, rh, w.b);
+          }
+          armed_r = rph + 1;
+          rph ^= 1;
+          for (int g = 0; g < w.heads && ok; ++g) {
+            const int ch = KV ? w.h + g : w.hk;
+            for (int t = 0; t < w.tiles; ++t) {
+              const int c0 = (w.c_first + t) * CB;
+              if (!(ok = mbar_wait(&cempty[cs], cph ^ 1, ctl))) break;
+              // a ragged tile lands on craw; warp 2 cleans it and completes cfull
+              const bool ragged = w.ragged(t, nstream);
+              uint64_t* bar = ragged ? &craw[cs] : &cfull[cs];
+              mbar_arrive_expect_tx(bar, Lay::load_bytes);
+  #pragma unroll
+              for (int c = 0; c < D / 64; ++c) {
+                if (Lay::S1) tma_load_4d(c1_s(cs) + c * (CB * 128), &p.tmC1, bar, c * 64, c0, ch, w.b);
+                if (Lay::S2) tma_load_4d(c2_s(cs) + c * (CB * 128), &p.tmC2, bar, c * 64, c0, ch, w.b);
+              }
+  #pragma unroll
+              for (int c = 0; c < DV / 64; ++c)
+                tma_load_4d(c3_s(cs) + c * (CB * 128), &p.tmC3, bar, w.half * DV + c * 64, c0,
+                            ch, w.b);
+              if (KV)
+                bulk_load(rec_s(cs),
+                          p.rec + (static_cast<size_t>(w.b * p.s.H + ch) * p.NQpad + c0) * kDiffRec,
+                          Lay::rec, bar);
+              armed_c[cs] = ragged ? 3 + ((rawph >> cs) & 1u) : cph + 1;
+              if (ragged) rawph ^= 1u << cs;
+              if (++cs == NST) {
+                cs = 0;
+                cph ^= 1;
+              }
+            }
+          }
+        }
+        if (!ok) {
+          // Aborting: let the copies already in flight land before the CTA exits.
+          volatile int zero = 0;
+          WaitCtl dctl{&zero, p.status, p.wait_limit_ns};
+          if (armed_r) mbar_wait(rfull, armed_r - 1, dctl);
+          for (int s = 0; s < NST; ++s)
+            if (armed_c[s])
+              mbar_wait(armed_c[s] > 2 ? &craw[s] : &cfull[s], (armed_c[s] - 1) & 1u, dctl);
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ UMMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idS = idesc_16<F16>(R, CB);
+        constexpr uint32_t idD = idesc_16<F16>(R, D, 0, 1);  // B = C, features contiguous
+        constexpr uint32_t idV = idesc_16<F16>(R, DV, 0, 1);
+        const uint64_t r1d = sdesc_sw128(smem_u32(r1_s), 16, 1024);
+        const uint64_t r2d = sdesc_sw128(smem_u32(r2_s), 16, 1024);
+        const uint64_t r3d = sdesc_sw128(smem_u32(r3_s), 16, 1024);
+        int cs = 0, cn = 0;  // stage of the step whose products are next, and of the one after
+        uint32_t rph = 0, cph = 0, seph = 0, xph = 0, oph = 0;
+        bool ok = true;
+        auto product = [&](uint32_t col, uint64_t rd, uint8_t* tile, int width) {
+          const uint64_t cd = sdesc_sw128(smem_u32(tile), 16, 1024);
+  #pragma unroll
+          for (int kk = 0; kk < width / 16; ++kk)
+            umma_bf16_ss(tmem + col, sdesc_advance(rd, (kk >> 2) * (R * 128) + (kk & 3) * 32),
+                         sdesc_advance(cd, (kk >> 2) * (CB * 128) + (kk & 3) * 32), idS, kk > 0);
+        };
+        auto issue_g = [&](int s) {
+          if (Lay::WG) product(kColG, r3d, c3_s(s), DV);
+          umma_commit(gfull);
+        };
+        // S of the step in stage cn, once its tiles are there and the warps have
+        // read the S before
+        bool first_step = true;  // of the whole run: nothing was read before
+        auto issue_s = [&]() -> bool {
+          if (!mbar_wait(&cfull[cn], cph, ctl)) return false;
+          if (!first_step) {
+            if (!mbar_wait(sempty, seph, ctl)) return false;
+            seph ^= 1;
+          }
+          first_step = false;
+          tc_fence_after();
+          if (Lay::S1) product(0, r1d, c1_s(cn), D);
+          if (Lay::S2) product(kColS2, r2d, c2_s(cn), D);
+          umma_commit(sfull);
+          if (++cn == NST) {
+            cn = 0;
+            cph ^= 1;
+          }
+          return true;
+        };
+        while (ok && sched.next(u)) {
+          const BwdUnit w = decode<PASS>(p, u);
+          if (w.tiles == 0) continue;
+          if (!(ok = mbar_wait(rfull, rph, ctl))) break;
+          rph ^= 1;
+          const int steps = w.heads * w.tiles;
+          if (!(ok = issue_s())) break;
+          issue_g(cs);
+          for (int t = 0; t < steps; ++t) {
+            if (t + 1 < steps && !(ok = issue_s())) break;
+            if (!(ok = mbar_wait(xfull, xph, ctl))) break;
+            xph ^= 1;
+            if (t == 0) {
+              if (!(ok = mbar_wait(oempty, oph ^ 1, ctl))) break;
+              oph ^= 1;
+            }
+            tc_fence_after();
+            const uint64_t c1m = sdesc_sw128(smem_u32(c1_s(cs)), CB * 128, 1024);
+            const uint64_t c2m = sdesc_sw128(smem_u32(c2_s(cs)), CB * 128, 1024);
+            const uint64_t c3m = sdesc_sw128(smem_u32(c3_s(cs)), CB * 128, 1024);
+  #pragma unroll
+            for (int kk = 0; kk < CB / 16; ++kk) {
+              const uint32_t acc = t > 0 || kk > 0;
+              if (Lay::X1)
+                umma_bf16_ts(tmem + Lay::o1, tmem + kColX1 + kk * 8, sdesc_advance(c1m, kk * 2048), idD, acc);
+              if (Lay::X2)
+                umma_bf16_ts(tmem + Lay::o2, tmem + kColX2 + kk * 8, sdesc_advance(c2m, kk * 2048), idD, acc);
+              if (Lay::WV)  // A over G, or (dV alone) in X1's place
+                umma_bf16_ts(tmem + Lay::o3, tmem + (Lay::WG ? kColG + kk * 16 : kColX1 + kk * 8),
+                             sdesc_advance(c3m, kk * 2048), idV, acc);
+            }
+            umma_commit(&cempty[cs]);
+            if (++cs == NST) cs = 0;
+            if (t + 1 < steps) issue_g(cs);
+          }
+          if (!ok) break;
+          umma_commit(ofull);
+          umma_commit(rempty);
+        }
+        umma_commit(drain);
+        volatile int zero = 0;
+        WaitCtl dctl{&zero, p.status, p.wait_limit_ns};
+        mbar_wait(drain, 0, dctl);
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ ragged tiles
+      int item = 0;  // ring items before this head of this unit
+      uint32_t rawph = 0;
+      bool ok = true;
+      while (ok && sched.next(u)) {
+        const BwdUnit w = decode<PASS>(p, u);
+        for (int g = 0; g < (w.tiles ? w.heads : 0) && ok; ++g, item += w.tiles) {
+          // only the first and the last tile can be ragged
+          for (int e = 0; e < (w.tiles > 1 ? 2 : 1); ++e) {
+            const int t = e ? w.tiles - 1 : 0;
+            if (!w.ragged(t, nstream)) continue;
+            const int s = static_cast<int>((static_cast<unsigned>(item) + t) % NST), c0 = (w.c_first + t) * CB;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&craw[s], (rawph >> s) & 1u, ctl)))) break;
+            rawph ^= 1u << s;
+            const int lo = max(0, w.lo - c0), hi = min(CB, max(0, w.hi - c0));
+            auto clean = [&](uint8_t* tile, int chunks) {
+              if (lo > 0) zero_tile_rows(tile, chunks, CB, 0, lo, lane);
+              if (hi < CB) zero_tile_rows(tile, chunks, CB, hi, CB, lane);
+            };
+            if (Lay::S1) clean(c1_s(s), D / 64);
+            if (Lay::S2) clean(c2_s(s), D / 64);
+            clean(c3_s(s), DV / 64);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&cfull[s]);
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int PASS, int D, int DV, int SEL, bool F16>
+cudaError_t launch_t(const DiffBwdParams& p, int num_sms, cudaStream_t stream) {
+  using Lay = BwdLay<PASS, D, DV, SEL>;
+  auto kern = streamkl_diff_bwd_kernel<PASS, D, DV, SEL, F16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::alloc);
+  if (e != cudaSuccess) return e;
+  const int nrows = PASS == kDiffKV ? p.s.NK : p.s.NQ;
+  const int units = p.s.B * (PASS == kDiffKV ? p.s.HK : p.s.H) * ((nrows + R - 1) / R) * p.nhalf;
+  kern<<<units < num_sms ? units : num_sms, NTHREADS, Lay::alloc, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <bool F16>
+cudaError_t launch_type(const DiffBwdParams& p, DiffPass pass, int d, int dv, int sel, int num_sms,
+                        cudaStream_t stream) {
+  if (pass == kDiffKV) {
+    if (d == 64 && dv == 64 && sel == 7) return launch_t<kDiffKV, 64, 64, 7, F16>(p, num_sms, stream);
+    if (d == 64 && dv == 128 && sel == 7) return launch_t<kDiffKV, 64, 128, 7, F16>(p, num_sms, stream);
+    if (d == 128 && dv == 128 && sel == 3) return launch_t<kDiffKV, 128, 128, 3, F16>(p, num_sms, stream);
+    if (d == 128 && dv == 256 && sel == 1) return launch_t<kDiffKV, 128, 256, 1, F16>(p, num_sms, stream);
+    if (d == 128 && dv == 256 && sel == 2) return launch_t<kDiffKV, 128, 256, 2, F16>(p, num_sms, stream);
+    if (d == 128 && sel == 4) return launch_t<kDiffKV, 128, 128, 4, F16>(p, num_sms, stream);
+  } else {
+    if (d == 64 && dv == 64 && sel == 3) return launch_t<kDiffQ, 64, 64, 3, F16>(p, num_sms, stream);
+    if (d == 64 && dv == 128 && sel == 3) return launch_t<kDiffQ, 64, 128, 3, F16>(p, num_sms, stream);
+    if (d == 128 && dv == 128 && sel == 3) return launch_t<kDiffQ, 128, 128, 3, F16>(p, num_sms, stream);
+    if (d == 128 && dv == 256 && sel == 1) return launch_t<kDiffQ, 128, 256, 1, F16>(p, num_sms, stream);
+    if (d == 128 && dv == 256 && sel == 2) return launch_t<kDiffQ, 128, 256, 2, F16>(p, num_sms, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// One warp per query row: D2 = <dO, O2>, D1 = <dO, O> + lam D2 (O = O1 - lam O2).
+// Reads dO, O, O2 once and is bound by HBM.
+template <bool F16>
+__global__ void __launch_bounds__(256) streamkl_diff_prep_kernel(const DiffPrepParams p) {
+  const int lane = threadIdx.x & 31;
+  const long long rows = static_cast<long long>(p.s.B) * p.s.H * p.NQpad;
+  const long long nw = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+  for (long long r = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+       r < rows; r += nw) {
+    const int i = static_cast<int>(r % p.NQpad);
+    const long long bh = r / p.NQpad;
+    const int b = static_cast<int>(bh / p.s.H), h = static_cast<int>(bh % p.s.H);
+    const Lens l = diff_lens(p.s, b);
+    const bool seen = i < l.q && l.k > 0 && (!p.s.causal || i + l.k - l.q >= 0);
+    float f[kDiffRec] = {-INFINITY, -INFINITY, 0.f, 0.f, 0.f};
+    if (seen) {
+      const uint16_t* g = static_cast<const uint16_t*>(p.dO) + b * p.sdo.b + h * p.sdo.h + i * p.sdo.n;
+      const long long oo = b * p.so.b + h * p.so.h + i * p.so.n;
+      const uint16_t* o = static_cast<const uint16_t*>(p.O) + oo;
+      const uint16_t* o2 = static_cast<const uint16_t*>(p.O2) + oo;
+      float d = 0.f, d2 = 0.f;
+      for (int c = lane * 8; c < p.dv; c += 256) {
+        const uint4 x = *reinterpret_cast<const uint4*>(g + c);
+        const uint4 y = *reinterpret_cast<const uint4*>(o + c);
+        const uint4 z = *reinterpret_cast<const uint4*>(o2 + c);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w},
+                       zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 a = unpack2<F16>(xs[k]), e = unpack2<F16>(ys[k]), e2 = unpack2<F16>(zs[k]);
+          d = fmaf(a.x, e.x, fmaf(a.y, e.y, d));
+          d2 = fmaf(a.x, e2.x, fmaf(a.y, e2.y, d2));
+        }
+      }
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) {
+        d += __shfl_xor_sync(0xffffffffu, d, s);
+        d2 += __shfl_xor_sync(0xffffffffu, d2, s);
+      }
+      const float lam = load_lam(p.lam, b, h, i, F16);
+      const long long v = bh * p.s.NQ + i;
+      f[0] = -p.LSE1[v] * kLog2e;
+      f[1] = -p.LSE2[v] * kLog2e;
+      f[2] = fmaf(lam, d2, d);
+      f[3] = d2;
+      f[4] = lam;
+    }
+    float* dst = p.rec + (bh * p.NQpad + (i / CB) * CB) * kDiffRec + i % CB;
+    if (lane < kDiffRec) {
+      const float val = lane == 0 ? f[0] : lane == 1 ? f[1] : lane == 2 ? f[2] : lane == 3 ? f[3] : f[4];
+      dst[lane * CB] = val;
+    }
+  }
+}
+
+// One block per element of dlam: -sum of D2 over the rows it is broadcast over,
+// each thread a strided share in order, then a tree: the same sum every time.
+__global__ void __launch_bounds__(512) streamkl_diff_lam_kernel(const DiffLamParams p) {
+  __shared__ float part[16];
+  const long long e = blockIdx.x;
+  const int n0 = static_cast<int>(e % p.en), h0 = static_cast<int>(e / p.en % p.eh),
+            b0 = static_cast<int>(e / p.en / p.eh);
+  const int nb = p.eb == 1 ? p.B : 1, nh = p.eh == 1 ? p.H : 1, nn = p.en == 1 ? p.NQ : 1;
+  const long long total = static_cast<long long>(nb) * nh * nn;
+  float s = 0.f;
+  for (long long k = threadIdx.x; k < total; k += blockDim.x) {
+    const int i = (p.en == 1 ? 0 : n0) + static_cast<int>(k % nn);
+    const long long q = k / nn;
+    const long long h = (p.eh == 1 ? 0 : h0) + q % nh, b = (p.eb == 1 ? 0 : b0) + q / nh;
+    s += p.rec[((b * p.H + h) * p.NQpad + (i / CB) * CB + 0) * kDiffRec + 3 * CB + i % CB];
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.f;
+    for (int k = 0; k < static_cast<int>(blockDim.x >> 5); ++k) s += part[k];
+    if (p.f32) static_cast<float*>(p.out)[e] = -s;
+    else if (p.f16) static_cast<__half*>(p.out)[e] = __float2half_rn(-s);
+    else static_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16_rn(-s);
+  }
+}
+
+// dlam of every row by itself (lam has an element per row): one thread a row.
+__global__ void __launch_bounds__(256) streamkl_diff_lam_rows_kernel(const DiffLamParams p) {
+  const long long total = static_cast<long long>(p.B) * p.H * p.NQ;
+  for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < total;
+       e += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const int i = static_cast<int>(e % p.NQ);
+    const long long bh = e / p.NQ;
+    const float s = -p.rec[(bh * p.NQpad + (i / CB) * CB) * kDiffRec + 3 * CB + i % CB];
+    if (p.f32) static_cast<float*>(p.out)[e] = s;
+    else if (p.f16) static_cast<__half*>(p.out)[e] = __float2half_rn(s);
+    else static_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16_rn(s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_diff_bwd(const DiffBwdParams& p, DiffPass pass, int d, int dv, int sel, bool f16,
+                            int num_sms, cudaStream_t stream) {
+  return f16 ? launch_type<true>(p, pass, d, dv, sel, num_sms, stream)
+             : launch_type<false>(p, pass, d, dv, sel, num_sms, stream);
+}
+
+cudaError_t launch_diff_prep(const DiffPrepParams& p, int num_sms, cudaStream_t stream) {
+  const long long blocks = (static_cast<long long>(p.s.B) * p.s.H * p.NQpad + 7) / 8;
+  const int grid = static_cast<int>(blocks < num_sms * 8ll ? blocks : num_sms * 8ll);
+  if (p.f16) streamkl_diff_prep_kernel<true><<<grid, 256, 0, stream>>>(p);
+  else streamkl_diff_prep_kernel<false><<<grid, 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_diff_lam(const DiffLamParams& p, cudaStream_t stream) {
+  const long long n = static_cast<long long>(p.eb) * p.eh * p.en;
+  if (p.eb == p.B && p.eh == p.H && p.en == p.NQ) {
+    const long long blocks = (n + 255) / 256;
+    streamkl_diff_lam_rows_kernel<<<static_cast<int>(blocks < 2048 ? blocks : 2048), 256, 0, stream>>>(p);
+  } else {
+    streamkl_diff_lam_kernel<<<static_cast<unsigned>(n), 512, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace skl

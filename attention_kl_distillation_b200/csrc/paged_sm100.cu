@@ -1,0 +1,595 @@
+// paged_sm100.cu -- single-token attention over a paged cache, through one
+// softmax map or the difference of two, and the write of new rows into pages.
+//
+//   O[b,h] = softmax(s1 Q1 K1^T) V  [ - lam softmax(s2 Q2 K2^T) V ]
+//
+// over the first lens[b] tokens of sequence b; token t lives in row t mod
+// page_size of page table[b][t / page_size].
+//
+// What bounds it: every cached row is read once, 2 (maps d + dv) bytes, for
+// 2 g (maps d + dv) FLOP by the g query heads that share it: 8 FLOP a byte at
+// g = 8.  That is HBM, by a factor of 30 under the tensor pipe, so the products
+// use warp-level mma with the keys on M and up to 8 query heads on N (no
+// padding of 8 heads to 128 rows) and each warp streams its own keys through
+// cp.async without a barrier among warps.
+//
+// Work split: a tile is 16 keys per team of warps, 128 (dv = 256: 64) per CTA.
+// The tiles of all sequences and key heads form one line, cut into equal
+// stretches, one per CTA: lengths may differ by any factor and every CTA still
+// reads the same number of rows.  The cut is computed on the device from lens,
+// so a captured graph stays right when lengths change.  A stretch may hold
+// several whole sequences (written at once) and a part of one at either end
+// (state to the workspace, joined by a second kernel in a fixed order).
+#include "diff_sm100.cuh"
+
+namespace skl {
+namespace {
+
+constexpr int KT = 16;       // keys per team and tile
+constexpr int NW = 8;        // warps per CTA
+constexpr int HB = 8;        // query heads per work item (mma N)
+constexpr int kMaxBatch = 4096;
+constexpr float kSlack = 8.f;  // a reference grows only by more than this (log2)
+
+template <int D, int DV, int MAPS>
+struct PagedLay {
+  static constexpr int WPT = DV > 128 ? 2 : 1;  // warps per team: each owns <= 128 value columns
+  static constexpr int TEAMS = NW / WPT;
+  static constexpr int DVW = DV / WPT;
+  static constexpr int MT = DVW / 16;           // value m-tiles per warp
+  static constexpr int TILE = KT * TEAMS;       // keys per CTA tile
+  static constexpr int k_bytes = KT * D * 2;
+  static constexpr int v_bytes = KT * DV * 2;
+  static constexpr int stage = MAPS * k_bytes + v_bytes;
+  static constexpr int fit = 196608 / (stage * TEAMS);
+  static constexpr int NST = fit > 6 ? 6 : fit;
+  static constexpr int NREG = MAPS * MT * 4;    // output registers per lane
+  static constexpr int ring = NST * stage * TEAMS;
+  static constexpr int buf = 2 * 32 * (NREG + 4 * MAPS) * 4;  // two warps' states
+  static constexpr int buf_off = ring;
+  static constexpr int mask_off = buf_off + buf;
+  static constexpr int cum_off = mask_off + NST * TEAMS * 4;
+  static constexpr int alloc(int B) { return cum_off + (B + 1) * 4; }
+  static_assert(NST >= 2, "ring too shallow");
+  static_assert(cum_off + (kMaxBatch + 1) * 4 <= 232448, "shared memory budget exceeded");
+  // Workspace of one stretch end: outputs and (m, l) per map and head, in the
+  // fragment order of the warps of a team.
+  static constexpr int slot_floats = WPT * 32 * (NREG + 4 * MAPS);
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Tokens of sequence b that are attended to: lens[b] within the table.
+__device__ __forceinline__ int paged_len(const PagedParams& p, int b) {
+  const long long most = static_cast<long long>(p.max_pages) * p.page_size;
+  const int n = max(p.lens[b], 0);
+  if (n > most) {
+    atomicCAS(p.status, 0, static_cast<int>(STREAMKL_EDEVICE));
+    return static_cast<int>(most);
+  }
+  return n;
+}
+
+__device__ __forceinline__ long long stretch_start(long long total, int c, int n) {
+  return total * c / n;
+}
+
+// cum[b] = tiles of the work items of sequences before b; cum[B] the total.
+// Items of a sequence: (key head, block of HB query heads), each of its tiles.
+template <int TILE>
+__device__ void tile_line(const PagedParams& p, int items, int* cum, int* scratch) {
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int per = (p.B + nt - 1) / nt;
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  int s = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int t = (paged_len(p, b) + TILE - 1) / TILE * items;
+    cum[b + 1] = t;
+    s += t;
+  }
+  const int lane = tid & 31, warp = tid >> 5;
+  int x = s;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) scratch[warp] = x;
+  __syncthreads();
+  int base = x - s;
+  for (int w = 0; w < warp; ++w) base += scratch[w];
+  for (int b = b0; b < b1; ++b) {
+    base += cum[b + 1];
+    cum[b + 1] = base;
+  }
+  if (tid == 0) cum[0] = 0;
+  __syncthreads();
+}
+
+// A position on the line of tiles.
+struct Cursor {
+  int b, item, tile, ntiles;  // item within the sequence; ntiles of one item
+  __device__ __forceinline__ void seek(const int* cum, int B, int items, int t) {
+    int lo = 0, hi = B - 1;  // the sequence with cum[b] <= t < cum[b + 1]
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cum[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+    ntiles = (cum[b + 1] - cum[b]) / items;
+    item = (t - cum[b]) / ntiles;
+    tile = (t - cum[b]) % ntiles;
+  }
+  __device__ __forceinline__ void advance(const int* cum, int B, int items) {
+    if (++tile < ntiles) return;
+    tile = 0;
+    if (++item < items) return;
+    item = 0;
+    do ++b;
+    while (b < B && cum[b + 1] == cum[b]);
+    if (b < B) ntiles = (cum[b + 1] - cum[b]) / items;
+  }
+};
+
+// The state of one warp: outputs O^T (value row lane/4 (+8), heads 2c, 2c+1 of
+// c = lane mod 4) and per map and head the reference and the sum.
+template <int MAPS, int MT>
+struct State {
+  float o[MAPS][MT][4];
+  float m[MAPS][2], l[MAPS][2];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int t = 0; t < MAPS; ++t) {
+#pragma unroll
+      for (int k = 0; k < MT; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][k][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[t][e] = -INFINITY;
+        l[t][e] = 0.f;
+      }
+    }
+  }
+  // fragment-order image, one float per lane at a stride of 32
+  __device__ __forceinline__ void put(float* dst, int lane) const {
+    int k = 0;
+#pragma unroll
+    for (int t = 0; t < MAPS; ++t)
+#pragma unroll
+      for (int q = 0; q < MT; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[32 * k++ + lane] = o[t][q][e];
+#pragma unroll
+    for (int t = 0; t < MAPS; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        dst[32 * k++ + lane] = m[t][e];
+        dst[32 * k++ + lane] = l[t][e];
+      }
+  }
+  // joins another state's image: both sides rescaled to the larger reference
+  __device__ __forceinline__ void join(const float* src, int lane) {
+    const float* ml = src + 32 * (MAPS * MT * 4);
+#pragma unroll
+    for (int t = 0; t < MAPS; ++t) {
+      float fa[2], fb[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float om = ml[32 * ((t * 2 + e) * 2) + lane], ol = ml[32 * ((t * 2 + e) * 2 + 1) + lane];
+        const float n = fmaxf(m[t][e], om);
+        // a side that saw nothing has m = -inf and weight 0
+        fa[e] = m[t][e] == -INFINITY ? 0.f : ex2(m[t][e] - n);
+        fb[e] = om == -INFINITY ? 0.f : ex2(om - n);
+        l[t][e] = fmaf(l[t][e], fa[e], ol * fb[e]);
+        m[t][e] = n;
+      }
+#pragma unroll
+      for (int q = 0; q < MT; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[t][q][e] = fmaf(o[t][q][e], fa[e & 1], src[32 * ((t * MT + q) * 4 + e) + lane] * fb[e & 1]);
+    }
+  }
+  // O_1/l_1 - lam O_2/l_2 of the heads first..first+HB-1 below `heads`
+  template <bool F16>
+  __device__ __forceinline__ void finish(const PagedParams& p, int b, int head0, int heads, int col0,
+                                         int lane) const {
+    float inv[MAPS][2];
+#pragma unroll
+    for (int t = 0; t < MAPS; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) inv[t][e] = l[t][e] > 0.f ? 1.f / l[t][e] : 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int k = (lane & 3) * 2 + e;
+      if (k >= heads) continue;
+      const int h = head0 + k;
+      const float f1 = inv[0][e];
+      float f2 = 0.f;
+      if (MAPS == 2) f2 = -inv[MAPS - 1][e] * load_lam(p.lam, b, h, 0, F16);
+      uint16_t* dst = static_cast<uint16_t*>(p.O) + b * p.o_b + h * p.o_h + col0 + (lane >> 2);
+#pragma unroll
+      for (int q = 0; q < MT; ++q) {
+        float x = o[0][q][e] * f1, y = o[0][q][e + 2] * f1;
+        if (MAPS == 2) {
+          x = fmaf(o[MAPS - 1][q][e], f2, x);
+          y = fmaf(o[MAPS - 1][q][e + 2], f2, y);
+        }
+        const uint32_t w = pack2<F16>(x, y);
+        dst[q * 16] = static_cast<uint16_t>(w);
+        dst[q * 16 + 8] = static_cast<uint16_t>(w >> 16);
+      }
+    }
+  }
+};
+
+template <int D, int DV, int MAPS, bool F16>
+__global__ void __launch_bounds__(NW * 32, 1)
+    streamkl_paged_kernel(const __grid_constant__ PagedParams p) {
+  using Lay = PagedLay<D, DV, MAPS>;
+  constexpr int NST = Lay::NST, WPT = Lay::WPT, MT = Lay::MT;
+  constexpr int KP = D / 8, VP = DV / 8;  // 16-byte pieces of a row
+  extern __shared__ __align__(128) uint8_t smem_paged[];
+  __shared__ int scratch[NW];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = warp / WPT, member = warp % WPT;
+  uint8_t* ring = smem_paged + team * (NST * Lay::stage);
+  float* buf = reinterpret_cast<float*>(smem_paged + Lay::buf_off);
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem_paged + Lay::mask_off) + team * NST;
+  int* cum = reinterpret_cast<int*>(smem_paged + Lay::cum_off);
+
+  const int g = p.H / p.HK, blocks = (g + HB - 1) / HB, items = p.HK * blocks;
+  tile_line<Lay::TILE>(p, items, cum, scratch);
+  const long long total = cum[p.B];
+  const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  const int c = blockIdx.x;
+
+  // sequences without a token: zeros
+  for (int b = c; b < p.B; b += gridDim.x) {
+    if (cum[b + 1] != cum[b]) continue;
+    for (int k = threadIdx.x; k < p.H * (DV / 8); k += blockDim.x)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O) + b * p.o_b + (k / VP) * p.o_h +
+                                (k % VP) * 8) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (c >= n) return;
+  const int t0 = static_cast<int>(stretch_start(total, c, n));
+  const int t1 = static_cast<int>(stretch_start(total, c + 1, n));
+
+  const uint32_t ring_a = smem_u32(ring);
+  // Issues the copies of tile `cur` into stage s; `cur_page` is lane r's page
+  // of row r (r < 16), looked up a tile ahead.
+  auto page_of = [&](const Cursor& cur) -> int {
+    const int tok = cur.tile * Lay::TILE + team * KT + (lane & 15);
+    if (tok >= min(p.lens[cur.b], p.max_pages * p.page_size)) return -1;
+    const int pg = p.table[cur.b * p.table_stride + tok / p.page_size];
+    if (pg < 0 || pg >= p.pages) {  // not a page: left out, and reported
+      atomicCAS(p.status, 0, static_cast<int>(STREAMKL_EDEVICE));
+      return -1;
+    }
+    return pg;
+  };
+  auto issue = [&](const Cursor& cur, int page, int s) {
+    const int tok = cur.tile * Lay::TILE + team * KT + (lane & 15);
+    const int slot = tok % p.page_size;
+    const uint32_t seen = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+    if (member == 0 && lane == 0) masks[s] = seen;
+    const int hk = cur.item / blocks;
+    auto copy = [&](const PagedCache& cache, uint32_t dst, int pieces) {
+      const uint16_t* base = static_cast<const uint16_t*>(cache.ptr) + hk * cache.head;
+#pragma unroll
+      for (int i = member; i < KT * pieces / 32; i += WPT) {
+        const int idx = i * 32 + lane, r = idx / pieces, q = idx % pieces;
+        const int pg = __shfl_sync(0xffffffffu, page, r);
+        const int sl = __shfl_sync(0xffffffffu, slot, r);
+        const uint16_t* src = base + (pg < 0 ? 0 : pg * cache.page + sl * cache.row + q * 8);
+        cp_async16(dst + r * pieces * 16 + ((q ^ (r & 7)) * 16), src, pg < 0 ? 0 : 16);
+      }
+    };
+    const uint32_t a = ring_a + s * Lay::stage;
+    copy(p.K1, a, KP);
+    if (MAPS == 2) copy(p.K2, a + Lay::k_bytes, KP);
+    copy(p.V, a + MAPS * Lay::k_bytes, VP);
+  };
+  auto team_sync = [&]() {
+    if (WPT == 1) __syncwarp();
+    else asm volatile("bar.sync %0, 64;" ::"r"(1 + team) : "memory");
+  };
+
+  Cursor ld, cur;
+  ld.seek(cum, p.B, items, t0);
+  cur = ld;
+  int tl = t0;  // next tile to be issued
+  int page = page_of(ld);
+  auto issue_next = [&](int s) {
+    if (tl < t1) {
+      issue(ld, page, s);
+      ++tl;
+      if (tl < t1) {
+        ld.advance(cum, p.B, items);
+        page = page_of(ld);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < NST - 1; ++s) issue_next(s);
+
+  State<MAPS, MT> st;
+  uint32_t qf[MAPS][D / 16][2];
+  auto load_q = [&]() {
+    const int hk = cur.item / blocks, k = (cur.item % blocks) * HB + (lane >> 2);
+#pragma unroll
+    for (int t = 0; t < MAPS; ++t) {
+      const uint16_t* q = t ? static_cast<const uint16_t*>(p.Q2) + cur.b * p.q2_b + (hk * g + k) * p.q2_h
+                            : static_cast<const uint16_t*>(p.Q1) + cur.b * p.q1_b + (hk * g + k) * p.q1_h;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          qf[t][kk][e] = k < g ? *reinterpret_cast<const uint32_t*>(q + kk * 16 + e * 8 + (lane & 3) * 2) : 0u;
+    }
+  };
+  int item_start = t0 - cur.tile;  // line position of the current item's first tile
+  st.clear();
+  load_q();
+
+  int s = 0;
+  for (int t = t0; t < t1; ++t) {
+    cp_async_wait<NST - 2>();
+    team_sync();
+    issue_next(s == 0 ? NST - 1 : s - 1);  // the stage read in the last round
+    const uint32_t a = ring_a + s * Lay::stage;
+    const uint32_t seen = masks[s];
+    uint32_t pf[MAPS][2];
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m) {
+      // S^T: keys lane/4 (+8), heads 2c, 2c+1
+      float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
+      const int r = lane & 15;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t af[4];
+        ldsm4(a + m * Lay::k_bytes + r * (D * 2) + (((kk * 2 + (lane >> 4)) ^ (r & 7)) * 16), af);
+        mma16816<F16>((kk & 1) ? sd : sc, af, qf[m][kk][0], qf[m][kk][1]);
+      }
+      const float cm = m ? p.c2 : p.c1;
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x[e] = ((seen >> ((lane >> 2) + (e >> 1) * 8)) & 1u) ? (sc[e] + sd[e]) * cm : -INFINITY;
+      float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+      if (__any_sync(0xffffffffu, mx[0] > st.m[m][0] + kSlack || mx[1] > st.m[m][1] + kSlack)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
+          const bool grow = mx[e] > st.m[m][e] + kSlack;
+          const float f = grow ? ex2(st.m[m][e] - mx[e]) : 1.f;
+          if (grow) st.m[m][e] = mx[e];
+          st.l[m][e] *= f;
+#pragma unroll
+          for (int q = 0; q < MT; ++q) {
+            st.o[m][q][e] *= f;
+            st.o[m][q][e + 2] *= f;
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float ref = st.m[m][e & 1] == -INFINITY ? 0.f : st.m[m][e & 1];
+        x[e] = ex2(x[e] - ref);
+        st.l[m][e & 1] += x[e];
+      }
+      // P^T as the B operand: heads on rows after the transposition
+      pf[m][0] = transpose8x8(pack2<F16>(x[0], x[1]));
+      pf[m][1] = transpose8x8(pack2<F16>(x[2], x[3]));
+    }
+#pragma unroll
+    for (int q = 0; q < MT; ++q) {
+      uint32_t vf[4];
+      const int r = (lane & 7) + ((lane >> 4) << 3);
+      const int piece = member * (Lay::DVW / 8) + q * 2 + ((lane >> 3) & 1);
+      ldsm4_t(a + MAPS * Lay::k_bytes + r * (DV * 2) + ((piece ^ (r & 7)) * 16), vf);
+#pragma unroll
+      for (int m = 0; m < MAPS; ++m) mma16816<F16>(st.o[m][q], vf, pf[m][0], pf[m][1]);
+    }
+    if (++s == NST) s = 0;
+
+    const bool item_ends = cur.tile + 1 == cur.ntiles;
+    if (item_ends || t + 1 == t1) {
+      // The warps' states of this item, joined in a fixed order.
+#pragma unroll
+      for (int m = 0; m < MAPS; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) st.l[m][e] += __shfl_xor_sync(0xffffffffu, st.l[m][e], d);
+      constexpr int image = 32 * (Lay::NREG + 4 * MAPS);
+      auto hand = [&](int from, int to, int count) {  // warps [from, from+count) to [to, ..)
+        __syncthreads();
+        if (warp >= from && warp < from + count) st.put(buf + (warp - from) * image, lane);
+        __syncthreads();
+        if (warp >= to && warp < to + count) st.join(buf + (warp - to) * image, lane);
+      };
+      hand(4, 0, 2);
+      hand(6, 2, 2);
+      hand(2, 0, 2);
+      if (WPT == 1) hand(1, 0, 1);
+      if (team == 0) {
+        const int hk = cur.item / blocks, first = (cur.item % blocks) * HB;
+        if (item_start >= t0 && item_ends) {
+          st.template finish<F16>(p, cur.b, hk * g + first, min(HB, g - first), member * Lay::DVW, lane);
+        } else {
+          // begun before this stretch: slot 2c; going on behind it: slot 2c + 1
+          const long long slot = 2ll * c + (item_start >= t0 ? 1 : 0);
+          st.put(p.part + slot * Lay::slot_floats + member * image, lane);
+        }
+      }
+      if (t + 1 < t1) {
+        cur.advance(cum, p.B, items);
+        item_start = t + 1;
+        st.clear();
+        load_q();
+      }
+    } else {
+      ++cur.tile;
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// Joins the parts of every item that stretches over several CTAs: block c looks
+// at the cut in front of stretch c and, if it is the first cut through its
+// item, joins the item's parts in order.
+template <int D, int DV, int MAPS, bool F16>
+__global__ void __launch_bounds__(NW * 32)
+    streamkl_paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
+  using Lay = PagedLay<D, DV, MAPS>;
+  extern __shared__ __align__(128) uint8_t smem_join[];
+  __shared__ int scratch[NW];
+  int* cum = reinterpret_cast<int*>(smem_join);
+  const int g = p.H / p.HK, blocks = (g + HB - 1) / HB, items = p.HK * blocks;
+  tile_line<Lay::TILE>(p, items, cum, scratch);
+  const long long total = cum[p.B];
+  const int n = static_cast<int>(min(static_cast<long long>(grid), total));
+  const int c = blockIdx.x + 1;
+  if (c >= n) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cut = static_cast<int>(stretch_start(total, c, n));
+  const int before = static_cast<int>(stretch_start(total, c - 1, n));
+  Cursor cur;
+  cur.seek(cum, p.B, items, cut);
+  const int start = cut - cur.tile, end = start + cur.ntiles;
+  if (start == cut || start < before) return;  // no item is cut here, or an earlier cut has it
+  if (warp >= Lay::WPT) return;
+  constexpr int image = 32 * (Lay::NREG + 4 * MAPS);
+  State<MAPS, Lay::MT> st;
+  st.clear();
+  st.join(p.part + (2ll * (c - 1) + 1) * Lay::slot_floats + warp * image, lane);
+  for (int k = c; k < n && stretch_start(total, k, n) < end; ++k)
+    st.join(p.part + 2ll * k * Lay::slot_floats + warp * image, lane);
+  const int hk = cur.item / blocks, first = (cur.item % blocks) * HB;
+  st.template finish<F16>(p, cur.b, hk * g + first, min(HB, g - first), warp * Lay::DVW, lane);
+}
+
+template <int D, int DV, int MAPS, bool F16>
+cudaError_t launch_t(const PagedParams& p, int num_sms, cudaStream_t stream) {
+  using Lay = PagedLay<D, DV, MAPS>;
+  auto kern = streamkl_paged_kernel<D, DV, MAPS, F16>;
+  const int smem = Lay::alloc(p.B);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<num_sms, NW * 32, smem, stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  streamkl_paged_join_kernel<D, DV, MAPS, F16>
+      <<<num_sms - 1, NW * 32, (p.B + 1) * 4, stream>>>(p, num_sms);
+  return cudaGetLastError();
+}
+
+template <int MAPS, bool F16>
+cudaError_t launch_dims(const PagedParams& p, int d, int dv, int num_sms, cudaStream_t stream) {
+  if (d == 64 && dv == 64) return launch_t<64, 64, MAPS, F16>(p, num_sms, stream);
+  if (d == 64 && dv == 128) return launch_t<64, 128, MAPS, F16>(p, num_sms, stream);
+  if (d == 128 && dv == 128) return launch_t<128, 128, MAPS, F16>(p, num_sms, stream);
+  if (d == 128 && dv == 256) return launch_t<128, 256, MAPS, F16>(p, num_sms, stream);
+  return cudaErrorInvalidValue;
+}
+
+// New rows into their slots, 16 bytes a thread and step; bound by HBM.  A
+// negative slot is skipped (a padded row); one past the cache is skipped and
+// reported.
+__global__ void __launch_bounds__(256) streamkl_paged_write_kernel(const __grid_constant__ PagedWriteParams p) {
+  const int w = blockIdx.y;
+  const int vecs = p.vecs[w], per = p.HK * vecs;
+  const long long total = static_cast<long long>(p.T) * per;
+  const long long slots = static_cast<long long>(p.pages) * p.page_size;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const int t = static_cast<int>(i / per), r = static_cast<int>(i - static_cast<long long>(t) * per);
+    const int h = r / vecs, v = r - h * vecs;
+    const long long slot = p.slots64 ? static_cast<const long long*>(p.slots)[t]
+                                     : static_cast<const int*>(p.slots)[t];
+    if (slot < 0) continue;
+    if (slot >= slots) {
+      atomicCAS(p.status, 0, static_cast<int>(STREAMKL_EDEVICE));
+      continue;
+    }
+    const long long page = slot / p.page_size, row = slot - page * p.page_size;
+    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.rows[w]) +
+                                                    t * p.row_t[w] + h * p.row_h[w] + v * 16);
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.caches[w]) + page * p.page[w] +
+                              row * p.slot[w] + h * p.head[w] + v * 16) = x;
+  }
+}
+
+}  // namespace
+
+size_t paged_workspace_bytes(int dv, int maps, int num_sms) {
+  // two slots per CTA; a slot holds HB heads' outputs and (m, l) pairs per lane
+  const int wpt = dv > 128 ? 2 : 1, mt = dv / wpt / 16;
+  return static_cast<size_t>(2 * num_sms) * wpt * 32 * (maps * mt * 4 + 4 * maps) * 4;
+}
+
+cudaError_t launch_paged(const PagedParams& p, int d, int dv, bool f16, int num_sms,
+                         cudaStream_t stream) {
+  if (p.B > kMaxBatch) return cudaErrorInvalidValue;
+  if (p.Q2) return f16 ? launch_dims<2, true>(p, d, dv, num_sms, stream)
+                       : launch_dims<2, false>(p, d, dv, num_sms, stream);
+  return f16 ? launch_dims<1, true>(p, d, dv, num_sms, stream)
+             : launch_dims<1, false>(p, d, dv, num_sms, stream);
+}
+
+cudaError_t launch_paged_write(const PagedWriteParams& p, int num_sms, cudaStream_t stream) {
+  int most = 0;
+  for (int i = 0; i < p.n; ++i) most = p.vecs[i] > most ? p.vecs[i] : most;
+  const long long blocks = (static_cast<long long>(p.T) * p.HK * most + 255) / 256;
+  const long long cap = 8ll * num_sms;
+  const dim3 grid(static_cast<unsigned>(blocks < cap ? blocks : cap), static_cast<unsigned>(p.n));
+  streamkl_paged_write_kernel<<<grid, 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace skl

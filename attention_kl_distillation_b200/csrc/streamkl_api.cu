@@ -16,6 +16,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "diff.h"
 #include "kernels.h"
 
 namespace {
@@ -251,6 +252,21 @@ BwdWorkspace bwd_workspace_layout(const streamkl_problem& pr) {
 }
 
 }  // namespace
+
+// What diff_api.cu shares with this file (declared in diff.h).
+namespace skl {
+streamkl_status api_device(int* num_sms, int** status) {
+  DeviceInfo* dev = nullptr;
+  const streamkl_status st = current_device(&dev);
+  if (st != STREAMKL_OK) return st;
+  *num_sms = dev->num_sms;
+  *status = dev->status;
+  return STREAMKL_OK;
+}
+unsigned long long api_wait_limit_ns() { return wait_limit_ns(); }
+void api_count_launches(int n) { g_launches.fetch_add(static_cast<uint64_t>(n)); }
+TensorMapEncode api_encode() { return g_encode; }
+}  // namespace skl
 
 extern "C" {
 

@@ -269,6 +269,139 @@ int streamkl_abi_version(void);
  */
 uint64_t streamkl_launch_count(void);
 
+/*
+ * ------------------------------------------------------------------------
+ * Differential attention and its serving form (no counterpart on the pages:
+ * the operators that use two softmax maps on values, beside the divergence
+ * above, which compares them).
+ *
+ *   x_t[i,j] = s_t * <Q_t[i], K_t[j]>,  P_t = softmax over the visible keys
+ *   O[i]     = sum_j (P_1[i,j] - lam[i] * P_2[i,j]) * V[j]
+ *
+ * Tensors are bf16 or fp16 (one type for all) and described by a pointer and
+ * the strides of their outer axes in elements; features are contiguous.
+ * Pointers are 16-byte aligned and strides are multiples of 8 elements (an
+ * axis of extent 1 may have any stride), none zero or negative.  Query head h
+ * reads key head h / (H / HK).  q_lens and k_lens (int32 [B], device memory,
+ * or NULL for full lengths) are the valid rows of a right-padded batch,
+ * clamped to 0..NQ and 0..NK: key j is visible from row i of batch b when
+ * i < q_lens[b], j < k_lens[b] and, if causal, j <= i + k_lens[b] - q_lens[b].
+ * Rows that see no key give O = 0, LSE = -inf and no gradient; rows of K, V,
+ * Q and dO outside the lengths may hold anything, NaN included, and their
+ * gradients are 0.
+ */
+typedef struct {
+  const void *ptr;
+  int64_t b, h, n; /* element strides of batch, head and row (a cache: page, head, row) */
+} streamkl_tensor;
+
+typedef enum { STREAMKL_BF16 = 0, STREAMKL_FP16 = 1 } streamkl_dtype;
+
+/*
+ * B, H, HK, NQ, NK >= 1, HK divides H; (d, dv) one of (64,64), (64,128),
+ * (128,128), (128,256); causal 0/1; lam_fp32: lam is stored in fp32 instead
+ * of dtype; s1, s2 <= 0 select 1/sqrt(d).
+ */
+typedef struct {
+  int B, H, HK, NQ, NK, d, dv, causal, dtype, lam_fp32;
+  float s1, s2;
+} streamkl_diff_problem;
+
+/*
+ * Forward.  lam: element (b, h, i) at b*lam.b + h*lam.h + i*lam.n; zero
+ * strides broadcast it.  O [B][H][NQ][dv].  O2 (map 2's own output, strides
+ * of O2 equal to O's), LSE1 and LSE2 (fp32 [B][H][NQ], contiguous) are the
+ * saved state of streamkl_diff_bwd; O2 == NULL, LSE1 == LSE2 == NULL skip them.
+ * Errors: EINVAL (null, unaligned or overlapping layout, sizes out of range,
+ * O2 strides other than O's), EUNSUPPORTED (other head widths or dtype, no
+ * sm_100 device), ECUDA.
+ */
+streamkl_status streamkl_diff_fwd(const streamkl_diff_problem *prob, const streamkl_tensor *Q1,
+                                  const streamkl_tensor *K1, const streamkl_tensor *Q2,
+                                  const streamkl_tensor *K2, const streamkl_tensor *V,
+                                  const streamkl_tensor *lam, const int *q_lens,
+                                  const int *k_lens, const streamkl_tensor *O,
+                                  const streamkl_tensor *O2, float *LSE1, float *LSE2,
+                                  streamkl_stream_t stream);
+
+/* Workspace bytes of streamkl_diff_bwd: five fp32 per query row.  0 on a bad problem. */
+size_t streamkl_diff_bwd_workspace_size(const streamkl_diff_problem *prob);
+
+/*
+ * Backward: gradients of sum <dO, O> from the forward's inputs and saved state.
+ * dQ1, dK1, dQ2, dK2, dV have the shapes of their inputs (any may be NULL); a
+ * key head's gradients are summed over the query heads that share it.  dlam,
+ * if not NULL, is contiguous in the shape that lam's nonzero strides span
+ * ([B or 1][H or 1][NQ or 1]) and of lam's type.  Accumulation is fp32 in a fixed
+ * order: results repeat bit for bit.  workspace: as the size above, 256-byte
+ * aligned, caller-owned, contents on entry do not matter.
+ * Errors: as streamkl_diff_fwd, plus EINVAL for a short or unaligned workspace or no
+ * output asked for.
+ */
+streamkl_status streamkl_diff_bwd(const streamkl_diff_problem *prob, const streamkl_tensor *dO,
+                                  const streamkl_tensor *Q1, const streamkl_tensor *K1,
+                                  const streamkl_tensor *Q2, const streamkl_tensor *K2,
+                                  const streamkl_tensor *V, const streamkl_tensor *lam,
+                                  const streamkl_tensor *O, const streamkl_tensor *O2,
+                                  const float *LSE1, const float *LSE2, const int *q_lens,
+                                  const int *k_lens, const streamkl_tensor *dQ1,
+                                  const streamkl_tensor *dK1, const streamkl_tensor *dQ2,
+                                  const streamkl_tensor *dK2, const streamkl_tensor *dV,
+                                  void *dlam, void *workspace, size_t ws_bytes,
+                                  streamkl_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over paged caches.  Caches are
+ * [pages][page_size][HK][width]: a streamkl_tensor whose b, h, n are the
+ * strides of page, key head and row.  Token t of sequence b is row t mod
+ * page_size of page table[b * table_stride + t / page_size]; page sizes need
+ * not be powers of two.  lens (int32 [B], device): tokens attended to; 0 gives
+ * O = 0; values past max_pages * page_size are cut there.  Entries of the
+ * table behind a sequence's length are not read.  An entry outside 0..pages-1
+ * is not followed: its tokens are left out.  Both that and a length past the
+ * table make streamkl_query_device_status return STREAMKL_EDEVICE.
+ * 1 <= B <= 4096, pages, page_size, max_pages >= 1.
+ */
+typedef struct {
+  int B, H, HK, d, dv, dtype, lam_fp32, pages, page_size, max_pages;
+  float s1, s2;
+} streamkl_paged_problem;
+
+/*
+ * maps 1: softmax(s1 Q1 K1^T) V; maps 2: minus lam softmax(s2 Q2 K2^T) V.
+ * Workspace bytes for either on the current device; 0 on a bad problem or no device.
+ */
+size_t streamkl_paged_workspace_size(const streamkl_paged_problem *prob, int maps);
+
+/*
+ * Q1 [B][H][d], O [B][H][dv] (n unused).  Q2 == K2 == lam == NULL: one map.
+ * lam: [B][H] by its strides (n unused).  workspace as above, 256-byte
+ * aligned, contents on entry do not matter.  The split of the sequences over
+ * the device is computed from lens on the device; results repeat bit for bit.
+ * Errors: EINVAL, EUNSUPPORTED, ECUDA as above.
+ */
+streamkl_status streamkl_paged_attn(const streamkl_paged_problem *prob, const streamkl_tensor *Q1,
+                                    const streamkl_tensor *K1, const streamkl_tensor *Q2,
+                                    const streamkl_tensor *K2, const streamkl_tensor *V,
+                                    const streamkl_tensor *lam, const int *table,
+                                    int64_t table_stride, const int *lens,
+                                    const streamkl_tensor *O, void *workspace, size_t ws_bytes,
+                                    streamkl_stream_t stream);
+
+/*
+ * Writes rows[k] [T][HK][widths[k]] (b unused, h and n the strides of head and
+ * row) into caches[k] for k < n <= 4 (one launch): row t goes to slot
+ * slots[t] = page * page_size + row.  slots: int32, or int64 with slots_int64.
+ * A negative slot is skipped; one past the cache is skipped and recorded
+ * (STREAMKL_EDEVICE).  Slots are distinct: of two rows with one slot either may
+ * stay, in pieces of 16 bytes.  Elements have 2 bytes; widths are multiples of 8.
+ * The rest of the caches is left as it was.
+ */
+streamkl_status streamkl_paged_write(int n, const streamkl_tensor *rows,
+                                     const streamkl_tensor *caches, const int *widths,
+                                     const void *slots, int slots_int64, int T, int HK, int pages,
+                                     int page_size, streamkl_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
