@@ -136,6 +136,7 @@ struct PagedParams {
   void* O;                   // [B][H][dv]
   long long o_b, o_h;
   int B, H, HK, pages, page_size, max_pages;
+  int page_shift;            // log2(page_size), or -1 when it is no power of two
   float c1, c2;
   float* part;               // workspace
   int* status;

@@ -367,6 +367,9 @@ streamkl_status streamkl_paged_attn(const streamkl_paged_problem* prob, const st
   p.pages = pr.pages;
   p.page_size = pr.page_size;
   p.max_pages = pr.max_pages;
+  p.page_shift = -1;
+  for (int k = 0; k < 31; ++k)
+    if (pr.page_size == 1 << k) p.page_shift = k;
   p.c1 = scale_of(pr.s1, pr.d) * kLog2e;
   p.c2 = scale_of(pr.s2, pr.d) * kLog2e;
   p.part = static_cast<float*>(workspace);

@@ -21,11 +21,12 @@
 // 16 bits and store those to TMEM, where they are the A operands of the output
 // products OUT += X C (C read with its features contiguous).
 // TMEM: S1 [0,64) S2 [64,128) G [128,192) X1 [192,224) X2 [224,256) OUT [256,..)
-// A replaces G (each 16-column group by the warpgroup that read it).
+// With X1 and X2 both there, A goes through shared memory (K-major, 128-byte
+// swizzle); in the dV-only pass it takes X1's place.
 //
-// S of step t+1 is issued as soon as the warps have read S of step t, so it and
-// the exponentials overlap; G of step t+1 is queued behind the products of step
-// t, and its commit therefore also says that X1, X2 and A may be overwritten.
+// The issuer's order is  G(t+1)  OUT(t)  S(t+2)  behind "X(t) is written": S of
+// a step and its exponentials, and G, are then under way while the step
+// before is contracted, and one step costs about the sum of its products.
 //
 // TMEM holds 256 output columns beside the 256 above, shared memory the
 // resident tiles and two stages. That decides the passes:
@@ -65,21 +66,32 @@ struct BwdLay {
   static constexpr int c2 = S2 ? CB * D * 2 : 0;
   static constexpr int c3 = CB * DV * 2;
   static constexpr int rec = KV ? CB * kDiffRec * 4 : 0;
-  static constexpr int load_bytes = c1 + c2 + c3 + rec;
-  static constexpr int stage = c1 + c2 + c3 + (rec ? 2048 : 0);
-  static constexpr int c_off = r1 + r2 + r3;
-  static constexpr int fit = (232448 - 1024 - 512 - c_off) / stage;
+  // dO (kKV) or V (kQ) rides in the ring with the other streamed tiles where the
+  // output products read it too (dV); where only G does, it has a ring of its
+  // own and is freed a step earlier, which at d = 128 makes room for a third stage.
+  static constexpr bool CR3 = WV;
+  static constexpr bool AS = WV && WG;             // A through shared memory
+  static constexpr int budget = 232448 - 1024 - 512;
+  static constexpr int a_off = r1 + r2 + r3;
+  static constexpr int v_off = a_off + (AS ? 2 * R * CB * 2 : 0);
+  static constexpr int stage = c1 + c2 + (CR3 ? c3 : 0);
+  static constexpr int load_bytes = stage + rec;
+  static constexpr int NSV = CR3 ? 0 : (v_off + 2 * c3 + 3 * (stage + rec) <= budget ? 2 : 1);
+  static constexpr int c_off = v_off + NSV * c3;
+  static constexpr int fit = (budget - c_off) / (stage + rec);
   static constexpr int NST = fit > 4 ? 4 : fit;
-  static constexpr int bar_off = c_off + NST * stage;
-  // cfull[NST] cempty[NST] craw[NST] rfull rempty sfull sempty gfull xfull ofull oempty drain
-  static constexpr int nbar = 3 * NST + 9;
+  static constexpr int rec_off = c_off + NST * stage;
+  static constexpr int bar_off = rec_off + NST * rec;
+  // cfull cempty craw [NST], vfull vempty vraw [NSV], rfull rempty sfull sempty
+  // gfull xfull xempty ofull oempty drain
+  static constexpr int nbar = 3 * NST + 3 * NSV + 10;
   static constexpr int misc_off = bar_off + nbar * 8;
   static constexpr int alloc = misc_off + 16 + 1024;
   static constexpr int o1 = kColOut;
   static constexpr int o2 = o1 + (X1 ? D : 0);
   static constexpr int o3 = o2 + (X2 ? D : 0);
   static_assert(o3 + (WV ? DV : 0) <= 512, "TMEM budget exceeded");
-  static_assert(NST >= 2, "streamed ring too shallow");
+  static_assert(NST >= 3, "streamed ring too shallow");
   static_assert(alloc <= 232448, "shared memory budget exceeded");
   static_assert(!(PASS == kDiffQ && WV), "dV belongs to the key pass");
 };
@@ -186,7 +198,7 @@ template <int PASS, int D, int DV, int SEL, bool F16>
 __global__ void __launch_bounds__(NTHREADS, 1)
     streamkl_diff_bwd_kernel(const __grid_constant__ DiffBwdParams p) {
   using Lay = BwdLay<PASS, D, DV, SEL>;
-  constexpr int NST = Lay::NST;
+  constexpr int NST = Lay::NST, NSV = Lay::NSV;
   constexpr bool KV = Lay::KV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -194,13 +206,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* cfull = reinterpret_cast<uint64_t*>(smem + Lay::bar_off);
   uint64_t* cempty = cfull + NST;
   uint64_t* craw = cempty + NST;  // a ragged tile has landed, to be cleaned
-  uint64_t* rfull = craw + NST;
+  uint64_t* vfull = craw + NST;   // the same for the ring of G's own tiles
+  uint64_t* vempty = vfull + NSV;
+  uint64_t* vraw = vempty + NSV;
+  uint64_t* rfull = vraw + NSV;
   uint64_t* rempty = rfull + 1;
   uint64_t* sfull = rempty + 1;  // S1, S2 of a step are in TMEM
   uint64_t* sempty = sfull + 1;  // ... and have been read
-  uint64_t* gfull = sempty + 1;  // G is in TMEM, and the products of the step before are done
-  uint64_t* xfull = gfull + 1;   // X1, X2, A are in TMEM
-  uint64_t* ofull = xfull + 1;
+  uint64_t* gfull = sempty + 1;  // G is in TMEM
+  uint64_t* xfull = gfull + 1;   // X1, X2, A are written (and G has been read)
+  uint64_t* xempty = xfull + 1;  // ... and have been contracted
+  uint64_t* ofull = xempty + 1;
   uint64_t* oempty = ofull + 1;
   uint64_t* drain = oempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::misc_off);
@@ -217,12 +233,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(&cempty[s], 1);
       mbar_init(&craw[s], 1);
     }
+    for (int s = 0; s < NSV; ++s) {
+      mbar_init(&vfull[s], 1);
+      mbar_init(&vempty[s], 1);
+      mbar_init(&vraw[s], 1);
+    }
     mbar_init(rfull, 1);
     mbar_init(rempty, 1);
     mbar_init(sfull, 1);
     mbar_init(sempty, 4 * NWG);
     mbar_init(gfull, 1);
     mbar_init(xfull, 4 * NWG);
+    mbar_init(xempty, 1);
     mbar_init(ofull, 1);
     mbar_init(oempty, 4 * NWG);
     mbar_init(drain, 1);
@@ -246,10 +268,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint8_t* r1_s = smem;
   uint8_t* r2_s = r1_s + Lay::r1;
   uint8_t* r3_s = r2_s + Lay::r2;
+  uint8_t* a_s = smem + Lay::a_off;
   auto c1_s = [&](int s) { return smem + Lay::c_off + s * Lay::stage; };
   auto c2_s = [&](int s) { return c1_s(s) + Lay::c1; };
-  auto c3_s = [&](int s) { return c1_s(s) + Lay::c1 + Lay::c2; };
-  auto rec_s = [&](int s) { return reinterpret_cast<float*>(c1_s(s) + Lay::c1 + Lay::c2 + Lay::c3); };
+  auto c3_s = [&](int s) {  // s counts the ring that holds it
+    return Lay::CR3 ? c1_s(s) + Lay::c1 + Lay::c2 : smem + Lay::v_off + s * Lay::c3;
+  };
+  auto rec_s = [&](int s) { return reinterpret_cast<float*>(smem + Lay::rec_off + s * Lay::rec); };
   const int nrows = KV ? p.s.NK : p.s.NQ;    // resident extent
   const int nstream = KV ? p.s.NQ : p.s.NK;  // streamed extent
   SnakeSched sched(p.s.B * (KV ? p.s.HK : p.s.H) * ((nrows + R - 1) / R) * p.nhalf);
@@ -264,17 +289,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int quarter = warp & 3;
     const int j = quarter * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    int cs = 0;
-    uint32_t cph = 0, sph = 0, gph = 0, oph = 0;
+    int cs = 0, gt = 0;  // gt: steps so far
+    uint32_t cph = 0, sph = 0, gph = 0, xph = 0, oph = 0;
     bool ok = true;
     while (ok && sched.next(u)) {
       const BwdUnit w = decode<PASS>(p, u);
-      const int row = w.r0 + j;  // key (kKV) or query (kQ)
+      const int mine = w.r0 + j;  // key (kKV) or query (kQ)
       const int off = w.l.k - w.l.q;
       float rec[kDiffRec] = {-INFINITY, -INFINITY, 0.f, 0.f, 0.f};
-      if (!KV && row < w.l.q && w.tiles) {
-        const float* r = p.rec + (static_cast<size_t>(w.b * p.s.H + w.h) * p.NQpad + (row / CB) * CB) *
-                                     kDiffRec + (row % CB);
+      if (!KV && mine < w.l.q && w.tiles) {
+        const float* r = p.rec + (static_cast<size_t>(w.b * p.s.H + w.h) * p.NQpad + (mine / CB) * CB) *
+                                     kDiffRec + (mine % CB);
 #pragma unroll
         for (int f = 0; f < kDiffRec; ++f) rec[f] = r[f * CB];
       }
@@ -302,26 +327,45 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         bool masked;
         if (KV) {
           masked = p.s.causal && c0 + off < w.r0 + R - 1;
-          if (p.s.causal) lo = row - off - cc;
+          if (p.s.causal) lo = mine - off - cc;
         } else {
           masked = c0 + CB > w.l.k || (p.s.causal && c0 + CB - 1 > w.r0 + off);
           hi = w.l.k - 1 - cc;
-          if (p.s.causal) hi = min(hi, row + off - cc);
+          if (p.s.causal) hi = min(hi, mine + off - cc);
         }
         const float* rr = KV ? rec_s(cs) + part * CPW : nullptr;
         if (masked)
           form_p<Lay, true, F16>(a, b, rr, rec, p.c1, p.c2, lo, hi);
         else
           form_p<Lay, false, F16>(a, b, rr, rec, p.c1, p.c2, lo, hi);
-        if (!(ok = mbar_wait(gfull, gph, ctl))) break;
-        gph ^= 1;
-        tc_fence_after();
+        const float2 NEG = make_float2(-1.f, -1.f);
+        uint32_t w1[CPW / 2], w2[CPW / 2], w3[CPW / 2];
+        auto pair = [](const uint32_t (&v)[CPW], int i) {
+          return make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+        };
+        if (Lay::WV) {
+#pragma unroll
+          for (int i = 0; i < CPW; i += 2) {
+            const float2 x = __ffma2_rn(pair(b, i), NEG, pair(a, i));
+            w3[i / 2] = pack2<F16>(x.x, x.y);
+          }
+        }
+        if (Lay::AS) {
+          // Row j, 16-byte pieces 2 part and 2 part + 1 of its 128 bytes.  The buffer
+          // was contracted two steps ago, which the last wait on xempty covered.
+          uint4* arow = reinterpret_cast<uint4*>(a_s + (gt & 1) * (R * CB * 2) + j * 128);
+          arow[(2 * part) ^ (j & 7)] = make_uint4(w3[0], w3[1], w3[2], w3[3]);
+          arow[(2 * part + 1) ^ (j & 7)] = make_uint4(w3[4], w3[5], w3[6], w3[7]);
+          fence_proxy_async_smem();
+        }
         if (Lay::WG) {
+          if (!(ok = mbar_wait(gfull, gph, ctl))) break;
+          gph ^= 1;
+          tc_fence_after();
           tmem_ld_32x32b_x16(tl + kColG + part * CPW, g);
           tmem_ld_wait();
           reg_fence(g);
         }
-        uint32_t w1[CPW / 2], w2[CPW / 2], w3[CPW / 2];
 #pragma unroll
         for (int q = 0; q < CPW; q += 4) {
           float4 d1 = make_float4(rec[2], rec[2], rec[2], rec[2]);
@@ -331,34 +375,29 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int i = q + 2 * e;
-            const float2 NEG = make_float2(-1.f, -1.f);
-            const float2 P1 = Lay::S1 ? make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])) : NEG;
-            const float2 P2 = Lay::S2 ? make_float2(__uint_as_float(b[i]), __uint_as_float(b[i + 1])) : NEG;
-            const float2 G = Lay::WG ? make_float2(__uint_as_float(g[i]), __uint_as_float(g[i + 1])) : NEG;
             if (Lay::X1) {
               const float2 d = e ? make_float2(d1.z, d1.w) : make_float2(d1.x, d1.y);
-              float2 x = __fmul2_rn(P1, __ffma2_rn(d, NEG, G));
+              const float2 x = __fmul2_rn(pair(a, i), __ffma2_rn(d, NEG, pair(g, i)));
               w1[i / 2] = pack2<F16>(x.x, x.y);
             }
             if (Lay::X2) {
               const float2 d = e ? make_float2(d2.z, d2.w) : make_float2(d2.x, d2.y);
-              float2 x = __fmul2_rn(P2, __ffma2_rn(G, NEG, d));
+              const float2 x = __fmul2_rn(pair(b, i), __ffma2_rn(pair(g, i), NEG, d));
               w2[i / 2] = pack2<F16>(x.x, x.y);
-            }
-            if (Lay::WV) {
-              const float2 x = __ffma2_rn(P2, NEG, P1);
-              w3[i / 2] = pack2<F16>(x.x, x.y);
             }
           }
         }
+        if (!(ok = mbar_wait(xempty, xph ^ 1, ctl))) break;
+        xph ^= 1;
+        tc_fence_after();
         if (Lay::X1) tmem_st_32x32b_x8(tl + kColX1 + part * (CPW / 2), w1);
         if (Lay::X2) tmem_st_32x32b_x8(tl + kColX2 + part * (CPW / 2), w2);
-        if (Lay::WV)
-          tmem_st_32x32b_x8(tl + (Lay::WG ? kColG + part * CPW : kColX1 + part * (CPW / 2)), w3);
+        if (Lay::WV && !Lay::AS) tmem_st_32x32b_x8(tl + kColX1 + part * (CPW / 2), w3);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(xfull);
+        ++gt;
         if (++cs == NST) {
           cs = 0;
           cph ^= 1;
@@ -371,19 +410,34 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         oph ^= 1;
         tc_fence_after();
       }
+      // Decoded again, from values that the compiler takes as new: what only the
+      // epilogue needs is then not held in registers through the steps.
+      int eu = u, ej = j, ep = part;
+      asm volatile("" : "+r"(eu), "+r"(ej), "+r"(ep));
+      const BwdUnit e = decode<PASS>(p, eu);
+      const int row = e.r0 + ej;
       const bool in_tensor = row < nrows;
       // rows behind their sequence, and rows that see nothing, get exact zeros
-      const bool live = steps > 0 && row < (KV ? w.l.k : w.l.q) &&
-                        (KV || !p.s.causal || row + off >= 0);
-      auto write = [&](void* dst, const Strides& st, uint32_t col, auto width_c, int first, float f) {
-        constexpr int W = decltype(width_c)::value / NWG;
-        const int h = KV ? w.hk : w.h;
-        uint16_t* o = static_cast<uint16_t*>(dst) + w.b * st.b + h * st.h + row * st.n + first + part * W;
-#pragma unroll
-        for (int c = 0; c < W; c += 16) {
-          uint32_t v[16];
+      const bool live = steps > 0 && row < (KV ? e.l.k : e.l.q) &&
+                        (KV || !p.s.causal || row + e.l.k - e.l.q >= 0);
+      const int h = KV ? e.hk : e.h;
+      // one output after the other, 16 columns at a time: a loop, so that its
+      // values do not take registers from the steps
+#pragma unroll 1
+      for (int o = 0; o < 3; ++o) {
+        const bool made = o == 0 ? Lay::X1 : o == 1 ? Lay::X2 : Lay::WV;
+        void* base = o == 0 ? p.out1 : o == 1 ? p.out2 : p.out3;
+        if (!made || !base) continue;
+        const Strides& st = o == 0 ? p.so1 : o == 1 ? p.so2 : p.so3;
+        const int cols = (o < 2 ? D : DV) / NWG, first = (o < 2 ? 0 : e.half * DV) + ep * cols;
+        const uint32_t col = (o == 0 ? Lay::o1 : o == 1 ? Lay::o2 : Lay::o3) + ep * cols;
+        const float f = o == 0 ? p.s1 : o == 1 ? p.s2 : 1.f;
+        uint16_t* dst = static_cast<uint16_t*>(base) + e.b * st.b + h * st.h + row * st.n + first;
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 16) {
+          uint32_t v[16] = {};
           if (steps > 0) {
-            tmem_ld_32x32b_x16(tl + col + part * W + c, v);
+            tmem_ld_32x32b_x16(tl + col + c, v);
             tmem_ld_wait();
             reg_fence(v);
           }
@@ -392,16 +446,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int k = 0; k < 8; ++k)
             x[k] = live ? pack2<F16>(__uint_as_float(v[2 * k]) * f, __uint_as_float(v[2 * k + 1]) * f) : 0u;
           if (in_tensor) {
-            *reinterpret_cast<uint4*>(o + c) = make_uint4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<uint4*>(o + c + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+            *reinterpret_cast<uint4*>(dst + c) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(x[4], x[5], x[6], x[7]);
           }
         }
-      };
-      using WD = std::integral_constant<int, D>;
-      using WDV = std::integral_constant<int, DV>;
-      if (Lay::X1 && p.out1) write(p.out1, p.so1, Lay::o1, WD{}, 0, p.s1);
-      if (Lay::X2 && p.out2) write(p.out2, p.so2, Lay::o2, WD{}, 0, p.s2);
-      if (Lay::WV && p.out3) write(p.out3, p.so3, Lay::o3, WDV{}, w.half * DV, 1.f);
+      }
       if (steps > 0) {
         tc_fence_before();
         __syncwarp();
@@ -413,9 +462,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (warp == 0) {
       // ------------------------------------------------------------ producer
       if (lane == 0) {
-        int cs = 0;
-        uint32_t rph = 0, cph = 0, rawph = 0;  // bit s of rawph: parity of craw[s]
-        uint32_t armed_r = 0, armed_c[NST] = {};  // last armed phase + 1; + 2 on craw
+        int cs = 0, vs = 0;
+        uint32_t rph = 0, cph = 0, vph = 0, rawph = 0, vrawph = 0;  // bit s of rawph: parity of craw[s]
+        uint32_t armed_r = 0, armed_c[NST] = {}, armed_v[NSV + 1] = {};  // last armed phase + 1; + 2 on raw
         bool ok = true;
         while (ok && sched.next(u)) {
           const BwdUnit w = decode<PASS>(p, u);
@@ -450,10 +499,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 if (Lay::S1) tma_load_4d(c1_s(cs) + c * (CB * 128), &p.tmC1, bar, c * 64, c0, ch, w.b);
                 if (Lay::S2) tma_load_4d(c2_s(cs) + c * (CB * 128), &p.tmC2, bar, c * 64, c0, ch, w.b);
               }
-  #pragma unroll
-              for (int c = 0; c < DV / 64; ++c)
-                tma_load_4d(c3_s(cs) + c * (CB * 128), &p.tmC3, bar, w.half * DV + c * 64, c0,
-                            ch, w.b);
+                auto load3 = [&](int slot, uint64_t* on) {
+#pragma unroll
+                for (int c = 0; c < DV / 64; ++c)
+                  tma_load_4d(c3_s(slot) + c * (CB * 128), &p.tmC3, on, w.half * DV + c * 64, c0, ch, w.b);
+              };
+              if (Lay::CR3) load3(cs, bar);
               if (KV)
                 bulk_load(rec_s(cs),
                           p.rec + (static_cast<size_t>(w.b * p.s.H + ch) * p.NQpad + c0) * kDiffRec,
@@ -463,6 +514,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               if (++cs == NST) {
                 cs = 0;
                 cph ^= 1;
+              }
+              if (!Lay::CR3) {
+                if (!(ok = mbar_wait(&vempty[vs], vph ^ 1, ctl))) break;
+                uint64_t* von = ragged ? &vraw[vs] : &vfull[vs];
+                mbar_arrive_expect_tx(von, Lay::c3);
+                load3(vs, von);
+                armed_v[vs] = ragged ? 3 + ((vrawph >> vs) & 1u) : vph + 1;
+                if (ragged) vrawph ^= 1u << vs;
+                if (++vs == NSV) {
+                  vs = 0;
+                  vph ^= 1;
+                }
               }
             }
           }
@@ -475,6 +538,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int s = 0; s < NST; ++s)
             if (armed_c[s])
               mbar_wait(armed_c[s] > 2 ? &craw[s] : &cfull[s], (armed_c[s] - 1) & 1u, dctl);
+          for (int s = 0; s < NSV; ++s)
+            if (armed_v[s])
+              mbar_wait(armed_v[s] > 2 ? &vraw[s] : &vfull[s], (armed_v[s] - 1) & 1u, dctl);
         }
       }
     } else if (warp == 1) {
@@ -486,19 +552,35 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const uint64_t r1d = sdesc_sw128(smem_u32(r1_s), 16, 1024);
         const uint64_t r2d = sdesc_sw128(smem_u32(r2_s), 16, 1024);
         const uint64_t r3d = sdesc_sw128(smem_u32(r3_s), 16, 1024);
+        const uint64_t ad = sdesc_sw128(smem_u32(a_s), 16, 1024);
         int cs = 0, cn = 0;  // stage of the step whose products are next, and of the one after
         uint32_t rph = 0, cph = 0, seph = 0, xph = 0, oph = 0;
         bool ok = true;
-        auto product = [&](uint32_t col, uint64_t rd, uint8_t* tile, int width) {
+        auto product = [&](uint32_t col, uint64_t resident, uint8_t* tile, int width) {
+          const uint64_t rd = here(resident);
           const uint64_t cd = sdesc_sw128(smem_u32(tile), 16, 1024);
   #pragma unroll
           for (int kk = 0; kk < width / 16; ++kk)
             umma_bf16_ss(tmem + col, sdesc_advance(rd, (kk >> 2) * (R * 128) + (kk & 3) * 32),
                          sdesc_advance(cd, (kk >> 2) * (CB * 128) + (kk & 3) * 32), idS, kk > 0);
         };
-        auto issue_g = [&](int s) {
-          if (Lay::WG) product(kColG, r3d, c3_s(s), DV);
+        int gt = 0;  // steps so far: A alternates between two buffers
+        int cg = 0;  // where the next G's streamed tile is
+        uint32_t vph = 0;
+        auto issue_g = [&]() -> bool {
+          if (!Lay::WG) return true;
+          if (!Lay::CR3) {
+            if (!mbar_wait(&vfull[cg], vph, ctl)) return false;
+            tc_fence_after();
+          }
+          product(kColG, r3d, c3_s(cg), DV);
           umma_commit(gfull);
+          if (!Lay::CR3) umma_commit(&vempty[cg]);
+          if (++cg == (Lay::CR3 ? NST : NSV)) {
+            cg = 0;
+            vph ^= 1;
+          }
+          return true;
         };
         // S of the step in stage cn, once its tiles are there and the warps have
         // read the S before
@@ -527,33 +609,47 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           rph ^= 1;
           const int steps = w.heads * w.tiles;
           if (!(ok = issue_s())) break;
-          issue_g(cs);
+          ok = issue_g();
+          if (!ok) break;
+          if (steps > 1) {
+            if (!(ok = issue_s())) break;
+          }
           for (int t = 0; t < steps; ++t) {
-            if (t + 1 < steps && !(ok = issue_s())) break;
             if (!(ok = mbar_wait(xfull, xph, ctl))) break;
             xph ^= 1;
+            tc_fence_after();
+            if (t + 1 < steps) {
+              ok = issue_g();
+              if (!ok) break;
+            }
             if (t == 0) {
               if (!(ok = mbar_wait(oempty, oph ^ 1, ctl))) break;
               oph ^= 1;
+              tc_fence_after();
             }
-            tc_fence_after();
             const uint64_t c1m = sdesc_sw128(smem_u32(c1_s(cs)), CB * 128, 1024);
             const uint64_t c2m = sdesc_sw128(smem_u32(c2_s(cs)), CB * 128, 1024);
             const uint64_t c3m = sdesc_sw128(smem_u32(c3_s(cs)), CB * 128, 1024);
-  #pragma unroll
+            const uint64_t a_d = sdesc_advance(here(ad), (gt & 1) * (R * CB * 2));
+#pragma unroll
             for (int kk = 0; kk < CB / 16; ++kk) {
               const uint32_t acc = t > 0 || kk > 0;
               if (Lay::X1)
                 umma_bf16_ts(tmem + Lay::o1, tmem + kColX1 + kk * 8, sdesc_advance(c1m, kk * 2048), idD, acc);
               if (Lay::X2)
                 umma_bf16_ts(tmem + Lay::o2, tmem + kColX2 + kk * 8, sdesc_advance(c2m, kk * 2048), idD, acc);
-              if (Lay::WV)  // A over G, or (dV alone) in X1's place
-                umma_bf16_ts(tmem + Lay::o3, tmem + (Lay::WG ? kColG + kk * 16 : kColX1 + kk * 8),
-                             sdesc_advance(c3m, kk * 2048), idV, acc);
+              if (Lay::AS)
+                umma_bf16_ss(tmem + Lay::o3, sdesc_advance(a_d, kk * 32), sdesc_advance(c3m, kk * 2048), idV, acc);
+              else if (Lay::WV)
+                umma_bf16_ts(tmem + Lay::o3, tmem + kColX1 + kk * 8, sdesc_advance(c3m, kk * 2048), idV, acc);
             }
             umma_commit(&cempty[cs]);
+            umma_commit(xempty);
+            ++gt;
             if (++cs == NST) cs = 0;
-            if (t + 1 < steps) issue_g(cs);
+            if (t + 2 < steps) {
+              if (!(ok = issue_s())) break;
+            }
           }
           if (!ok) break;
           umma_commit(ofull);
@@ -567,7 +663,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     } else if (warp == 2) {
       // ------------------------------------------------------------ ragged tiles
       int item = 0;  // ring items before this head of this unit
-      uint32_t rawph = 0;
+      uint32_t rawph = 0, vrawph = 0;
       bool ok = true;
       while (ok && sched.next(u)) {
         const BwdUnit w = decode<PASS>(p, u);
@@ -586,10 +682,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             };
             if (Lay::S1) clean(c1_s(s), D / 64);
             if (Lay::S2) clean(c2_s(s), D / 64);
-            clean(c3_s(s), DV / 64);
+            if (Lay::CR3) clean(c3_s(s), DV / 64);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&cfull[s]);
+            if (!Lay::CR3) {
+              const int v = static_cast<int>((static_cast<unsigned>(item) + t) % (NSV + Lay::CR3));
+              if (!(ok = __all_sync(0xffffffffu, mbar_wait(&vraw[v], (vrawph >> v) & 1u, ctl)))) break;
+              vrawph ^= 1u << v;
+              clean(c3_s(v), DV / 64);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&vfull[v]);
+            }
           }
         }
       }
@@ -637,58 +742,70 @@ cudaError_t launch_type(const DiffBwdParams& p, DiffPass pass, int d, int dv, in
   return cudaErrorInvalidValue;
 }
 
-// One warp per query row: D2 = <dO, O2>, D1 = <dO, O> + lam D2 (O = O1 - lam O2).
-// Reads dO, O, O2 once and is bound by HBM.
-template <bool F16>
+// Row records: D2 = <dO, O2>, D1 = <dO, O> + lam D2 (O = O1 - lam O2).  A block
+// takes 64 rows, DV / 8 lanes a row, so that every thread has its share of
+// dO, O and O2 (16 bytes of each, DV / 32 rows) in flight at once: bound by HBM.
+template <int DV, bool F16>
 __global__ void __launch_bounds__(256) streamkl_diff_prep_kernel(const DiffPrepParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long rows = static_cast<long long>(p.s.B) * p.s.H * p.NQpad;
-  const long long nw = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
-  for (long long r = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-       r < rows; r += nw) {
-    const int i = static_cast<int>(r % p.NQpad);
-    const long long bh = r / p.NQpad;
-    const int b = static_cast<int>(bh / p.s.H), h = static_cast<int>(bh % p.s.H);
+  constexpr int L = DV / 8, RPT = CB * L / 256;  // lanes a row, rows a thread
+  __shared__ float out[kDiffRec][CB];
+  const int steps = p.NQpad / CB, units = p.s.B * p.s.H * steps;
+  const int sub = threadIdx.x % L, r0 = threadIdx.x / L;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int bh = u / steps, i0 = (u - bh * steps) * CB;
+    const int b = bh / p.s.H, h = bh - b * p.s.H;
     const Lens l = diff_lens(p.s, b);
-    const bool seen = i < l.q && l.k > 0 && (!p.s.causal || i + l.k - l.q >= 0);
-    float f[kDiffRec] = {-INFINITY, -INFINITY, 0.f, 0.f, 0.f};
-    if (seen) {
-      const uint16_t* g = static_cast<const uint16_t*>(p.dO) + b * p.sdo.b + h * p.sdo.h + i * p.sdo.n;
-      const long long oo = b * p.so.b + h * p.so.h + i * p.so.n;
-      const uint16_t* o = static_cast<const uint16_t*>(p.O) + oo;
-      const uint16_t* o2 = static_cast<const uint16_t*>(p.O2) + oo;
-      float d = 0.f, d2 = 0.f;
-      for (int c = lane * 8; c < p.dv; c += 256) {
-        const uint4 x = *reinterpret_cast<const uint4*>(g + c);
-        const uint4 y = *reinterpret_cast<const uint4*>(o + c);
-        const uint4 z = *reinterpret_cast<const uint4*>(o2 + c);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w},
-                       zs[4] = {z.x, z.y, z.z, z.w};
+    uint4 x[RPT], y[RPT], z[RPT];
+    bool seen[RPT];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 a = unpack2<F16>(xs[k]), e = unpack2<F16>(ys[k]), e2 = unpack2<F16>(zs[k]);
-          d = fmaf(a.x, e.x, fmaf(a.y, e.y, d));
-          d2 = fmaf(a.x, e2.x, fmaf(a.y, e2.y, d2));
-        }
+    for (int k = 0; k < RPT; ++k) {
+      const int i = i0 + r0 + k * (256 / L);
+      seen[k] = i < l.q && l.k > 0 && (!p.s.causal || i + l.k - l.q >= 0);
+      x[k] = y[k] = z[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (seen[k]) {
+        const long long oo = b * p.so.b + h * p.so.h + i * p.so.n + sub * 8;
+        x[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dO) + b * p.sdo.b +
+                                               h * p.sdo.h + i * p.sdo.n + sub * 8);
+        y[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.O) + oo);
+        z[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.O2) + oo);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < RPT; ++k) {
+      const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, ys[4] = {y[k].x, y[k].y, y[k].z, y[k].w},
+                     zs[4] = {z[k].x, z[k].y, z[k].z, z[k].w};
+      float d = 0.f, d2 = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 a = unpack2<F16>(xs[e]), o = unpack2<F16>(ys[e]), o2 = unpack2<F16>(zs[e]);
+        d = fmaf(a.x, o.x, fmaf(a.y, o.y, d));
+        d2 = fmaf(a.x, o2.x, fmaf(a.y, o2.y, d2));
       }
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) {
+      for (int s = L / 2; s > 0; s >>= 1) {
         d += __shfl_xor_sync(0xffffffffu, d, s);
         d2 += __shfl_xor_sync(0xffffffffu, d2, s);
       }
-      const float lam = load_lam(p.lam, b, h, i, F16);
-      const long long v = bh * p.s.NQ + i;
-      f[0] = -p.LSE1[v] * kLog2e;
-      f[1] = -p.LSE2[v] * kLog2e;
-      f[2] = fmaf(lam, d2, d);
-      f[3] = d2;
-      f[4] = lam;
+      if (sub == 0) {
+        const int row = r0 + k * (256 / L), i = i0 + row;
+        float lam = 0.f, n1 = -INFINITY, n2 = -INFINITY;
+        if (seen[k]) {
+          const long long v = static_cast<long long>(bh) * p.s.NQ + i;
+          lam = load_lam(p.lam, b, h, i, F16);
+          n1 = -p.LSE1[v] * kLog2e;
+          n2 = -p.LSE2[v] * kLog2e;
+        }
+        out[0][row] = n1;
+        out[1][row] = n2;
+        out[2][row] = fmaf(lam, d2, d);
+        out[3][row] = d2;
+        out[4][row] = lam;
+      }
     }
-    float* dst = p.rec + (bh * p.NQpad + (i / CB) * CB) * kDiffRec + i % CB;
-    if (lane < kDiffRec) {
-      const float val = lane == 0 ? f[0] : lane == 1 ? f[1] : lane == 2 ? f[2] : lane == 3 ? f[3] : f[4];
-      dst[lane * CB] = val;
-    }
+    __syncthreads();
+    float* dst = p.rec + static_cast<long long>(u) * (CB * kDiffRec);
+    for (int k = threadIdx.x; k < CB * kDiffRec; k += 256) dst[k] = out[k / CB][k % CB];
+    __syncthreads();
   }
 }
 
@@ -744,10 +861,16 @@ cudaError_t launch_diff_bwd(const DiffBwdParams& p, DiffPass pass, int d, int dv
 }
 
 cudaError_t launch_diff_prep(const DiffPrepParams& p, int num_sms, cudaStream_t stream) {
-  const long long blocks = (static_cast<long long>(p.s.B) * p.s.H * p.NQpad + 7) / 8;
-  const int grid = static_cast<int>(blocks < num_sms * 8ll ? blocks : num_sms * 8ll);
-  if (p.f16) streamkl_diff_prep_kernel<true><<<grid, 256, 0, stream>>>(p);
-  else streamkl_diff_prep_kernel<false><<<grid, 256, 0, stream>>>(p);
+  const int units = p.s.B * p.s.H * (p.NQpad / CB);
+  const int grid = units < num_sms * 8 ? units : num_sms * 8;
+  auto run = [&](auto f16) {
+    constexpr bool F16 = decltype(f16)::value;
+    if (p.dv == 64) streamkl_diff_prep_kernel<64, F16><<<grid, 256, 0, stream>>>(p);
+    else if (p.dv == 128) streamkl_diff_prep_kernel<128, F16><<<grid, 256, 0, stream>>>(p);
+    else streamkl_diff_prep_kernel<256, F16><<<grid, 256, 0, stream>>>(p);
+  };
+  if (p.f16) run(std::true_type{});
+  else run(std::false_type{});
   return cudaGetLastError();
 }
 

@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // S_t of the keys at `tile`
         auto issue_s = [&](int t, uint8_t* tile) {
           const uint64_t kd = sdesc_sw128(smem_u32(tile), 16, 1024);
-          const uint64_t qd = t ? q2d : q1d;
+          const uint64_t qd = here(t ? q2d : q1d);
   #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t o = (kk >> 2) * (BK * 128) + (kk & 3) * 32;

@@ -27,6 +27,13 @@ __host__ __device__ constexpr uint32_t idesc_16(int M, int N, int a_mn = 0, int 
              : idesc_bf16(M, N, a_mn, b_mn);
 }
 
+// A descriptor as this point of the program computes it: keeps the compiler from
+// holding every product's descriptor of a loop in registers (and spilling them).
+__device__ __forceinline__ uint64_t here(uint64_t desc) {
+  asm volatile("" : "+l"(desc));
+  return desc;
+}
+
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (F16) {

@@ -29,6 +29,7 @@ constexpr int KT = 16;       // keys per team and tile
 constexpr int NW = 8;        // warps per CTA
 constexpr int HB = 8;        // query heads per work item (mma N)
 constexpr int kMaxBatch = 4096;
+constexpr int kBehind = -2147483647 - 1;
 constexpr float kSlack = 8.f;  // a reference grows only by more than this (log2)
 
 template <int D, int DV, int MAPS>
@@ -45,7 +46,7 @@ struct PagedLay {
   static constexpr int NST = fit > 6 ? 6 : fit;
   static constexpr int NREG = MAPS * MT * 4;    // output registers per lane
   static constexpr int ring = NST * stage * TEAMS;
-  static constexpr int buf = 2 * 32 * (NREG + 4 * MAPS) * 4;  // two warps' states
+  static constexpr int buf = 2 * 32 * (NREG + 4 * MAPS) * 4;  // two warps' states at a time
   static constexpr int buf_off = ring;
   static constexpr int mask_off = buf_off + buf;
   static constexpr int cum_off = mask_off + NST * TEAMS * 4;
@@ -54,7 +55,8 @@ struct PagedLay {
   static_assert(cum_off + (kMaxBatch + 1) * 4 <= 232448, "shared memory budget exceeded");
   // Workspace of one stretch end: outputs and (m, l) per map and head, in the
   // fragment order of the warps of a team.
-  static constexpr int slot_floats = WPT * 32 * (NREG + 4 * MAPS);
+  static constexpr int image = 32 * (NREG + 4 * MAPS);  // floats of one warp's state
+  static constexpr int slot_floats = WPT * image;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -149,9 +151,9 @@ __device__ void tile_line(const PagedParams& p, int items, int* cum, int* scratc
 
 // A position on the line of tiles.
 struct Cursor {
-  int b, item, tile, ntiles;  // item within the sequence; ntiles of one item
-  __device__ __forceinline__ void seek(const int* cum, int B, int items, int t) {
-    int lo = 0, hi = B - 1;  // the sequence with cum[b] <= t < cum[b + 1]
+  int b, item, tile, ntiles, len;  // item within the sequence; ntiles of one item
+  __device__ __forceinline__ void seek(const PagedParams& p, const int* cum, int items, int t) {
+    int lo = 0, hi = p.B - 1;  // the sequence with cum[b] <= t < cum[b + 1]
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (cum[mid] <= t) lo = mid;
@@ -161,15 +163,19 @@ struct Cursor {
     ntiles = (cum[b + 1] - cum[b]) / items;
     item = (t - cum[b]) / ntiles;
     tile = (t - cum[b]) % ntiles;
+    len = paged_len(p, b);
   }
-  __device__ __forceinline__ void advance(const int* cum, int B, int items) {
+  __device__ __forceinline__ void advance(const PagedParams& p, const int* cum, int items) {
     if (++tile < ntiles) return;
     tile = 0;
     if (++item < items) return;
     item = 0;
     do ++b;
-    while (b < B && cum[b + 1] == cum[b]);
-    if (b < B) ntiles = (cum[b + 1] - cum[b]) / items;
+    while (b < p.B && cum[b + 1] == cum[b]);
+    if (b < p.B) {
+      ntiles = (cum[b + 1] - cum[b]) / items;
+      len = paged_len(p, b);
+    }
   }
 };
 
@@ -266,6 +272,22 @@ struct State {
   }
 };
 
+// Joins the states of all warps into those of the first team, in a fixed order,
+// through a buffer of two warps' states.
+template <class Lay, class S>
+__device__ __forceinline__ void join_warps(S& st, float* buf, int warp, int lane) {
+  auto hand = [&](int from, int to, int count) {  // warps [from, from + count) to [to, ..)
+    __syncthreads();
+    if (warp >= from && warp < from + count) st.put(buf + (warp - from) * Lay::image, lane);
+    __syncthreads();
+    if (warp >= to && warp < to + count) st.join(buf + (warp - to) * Lay::image, lane);
+  };
+  hand(4, 0, 2);
+  hand(6, 2, 2);
+  hand(2, 0, 2);
+  if (Lay::WPT == 1) hand(1, 0, 1);
+}
+
 template <int D, int DV, int MAPS, bool F16>
 __global__ void __launch_bounds__(NW * 32, 1)
     streamkl_paged_kernel(const __grid_constant__ PagedParams p) {
@@ -281,6 +303,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   uint32_t* masks = reinterpret_cast<uint32_t*>(smem_paged + Lay::mask_off) + team * NST;
   int* cum = reinterpret_cast<int*>(smem_paged + Lay::cum_off);
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int g = p.H / p.HK, blocks = (g + HB - 1) / HB, items = p.HK * blocks;
   tile_line<Lay::TILE>(p, items, cum, scratch);
   const long long total = cum[p.B];
@@ -299,33 +322,35 @@ __global__ void __launch_bounds__(NW * 32, 1)
   const int t1 = static_cast<int>(stretch_start(total, c + 1, n));
 
   const uint32_t ring_a = smem_u32(ring);
-  // Issues the copies of tile `cur` into stage s; `cur_page` is lane r's page
-  // of row r (r < 16), looked up a tile ahead.
+  // Page and row of token tok; page sizes are mostly powers of two.
+  auto page_index = [&](int tok) { return p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size; };
+  auto page_row = [&](int tok) { return p.page_shift >= 0 ? tok & (p.page_size - 1) : tok % p.page_size; };
+  auto token = [&](const Cursor& cur) { return cur.tile * Lay::TILE + team * KT + (lane & 15); };
+  // Lane r (and r + 16) reads the table entry of row r a tile ahead of its use;
+  // what it holds is looked at only then.  kBehind: no such token.
   auto page_of = [&](const Cursor& cur) -> int {
-    const int tok = cur.tile * Lay::TILE + team * KT + (lane & 15);
-    if (tok >= min(p.lens[cur.b], p.max_pages * p.page_size)) return -1;
-    const int pg = p.table[cur.b * p.table_stride + tok / p.page_size];
-    if (pg < 0 || pg >= p.pages) {  // not a page: left out, and reported
-      atomicCAS(p.status, 0, static_cast<int>(STREAMKL_EDEVICE));
-      return -1;
-    }
-    return pg;
+    const int tok = token(cur);
+    return tok < cur.len ? p.table[cur.b * p.table_stride + page_index(tok)] : kBehind;
   };
+  // Issues the copies of tile `cur` into stage s.
   auto issue = [&](const Cursor& cur, int page, int s) {
-    const int tok = cur.tile * Lay::TILE + team * KT + (lane & 15);
-    const int slot = tok % p.page_size;
+    if (page != kBehind && (page < 0 || page >= p.pages)) {  // not a page: left out, and reported
+      atomicCAS(p.status, 0, static_cast<int>(STREAMKL_EDEVICE));
+      page = -1;
+    }
+    const int slot = page_row(token(cur));
     const uint32_t seen = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
     if (member == 0 && lane == 0) masks[s] = seen;
     const int hk = cur.item / blocks;
     auto copy = [&](const PagedCache& cache, uint32_t dst, int pieces) {
       const uint16_t* base = static_cast<const uint16_t*>(cache.ptr) + hk * cache.head;
+      const long long row = page * cache.page + slot * cache.row;  // of this lane's row
 #pragma unroll
       for (int i = member; i < KT * pieces / 32; i += WPT) {
         const int idx = i * 32 + lane, r = idx / pieces, q = idx % pieces;
-        const int pg = __shfl_sync(0xffffffffu, page, r);
-        const int sl = __shfl_sync(0xffffffffu, slot, r);
-        const uint16_t* src = base + (pg < 0 ? 0 : pg * cache.page + sl * cache.row + q * 8);
-        cp_async16(dst + r * pieces * 16 + ((q ^ (r & 7)) * 16), src, pg < 0 ? 0 : 16);
+        const long long off = __shfl_sync(0xffffffffu, row, r);
+        const bool ok = (seen >> r) & 1u;
+        cp_async16(dst + r * pieces * 16 + ((q ^ (r & 7)) * 16), base + (ok ? off + q * 8 : 0), ok ? 16 : 0);
       }
     };
     const uint32_t a = ring_a + s * Lay::stage;
@@ -339,7 +364,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   };
 
   Cursor ld, cur;
-  ld.seek(cum, p.B, items, t0);
+  ld.seek(p, cum, items, t0);
   cur = ld;
   int tl = t0;  // next tile to be issued
   int page = page_of(ld);
@@ -348,7 +373,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
       issue(ld, page, s);
       ++tl;
       if (tl < t1) {
-        ld.advance(cum, p.B, items);
+        ld.advance(p, cum, items);
         page = page_of(ld);
       }
     }
@@ -447,17 +472,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) st.l[m][e] += __shfl_xor_sync(0xffffffffu, st.l[m][e], d);
-      constexpr int image = 32 * (Lay::NREG + 4 * MAPS);
-      auto hand = [&](int from, int to, int count) {  // warps [from, from+count) to [to, ..)
-        __syncthreads();
-        if (warp >= from && warp < from + count) st.put(buf + (warp - from) * image, lane);
-        __syncthreads();
-        if (warp >= to && warp < to + count) st.join(buf + (warp - to) * image, lane);
-      };
-      hand(4, 0, 2);
-      hand(6, 2, 2);
-      hand(2, 0, 2);
-      if (WPT == 1) hand(1, 0, 1);
+      join_warps<Lay>(st, buf, warp, lane);
       if (team == 0) {
         const int hk = cur.item / blocks, first = (cur.item % blocks) * HB;
         if (item_start >= t0 && item_ends) {
@@ -465,11 +480,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
         } else {
           // begun before this stretch: slot 2c; going on behind it: slot 2c + 1
           const long long slot = 2ll * c + (item_start >= t0 ? 1 : 0);
-          st.put(p.part + slot * Lay::slot_floats + member * image, lane);
+          st.put(p.part + slot * Lay::slot_floats + member * Lay::image, lane);
         }
       }
       if (t + 1 < t1) {
-        cur.advance(cum, p.B, items);
+        cur.advance(p, cum, items);
         item_start = t + 1;
         st.clear();
         load_q();
@@ -483,36 +498,43 @@ __global__ void __launch_bounds__(NW * 32, 1)
 
 // Joins the parts of every item that stretches over several CTAs: block c looks
 // at the cut in front of stretch c and, if it is the first cut through its
-// item, joins the item's parts in order.
+// item, joins the item's parts: each team every TEAMS-th, then the teams.
 template <int D, int DV, int MAPS, bool F16>
 __global__ void __launch_bounds__(NW * 32)
     streamkl_paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
   using Lay = PagedLay<D, DV, MAPS>;
   extern __shared__ __align__(128) uint8_t smem_join[];
   __shared__ int scratch[NW];
-  int* cum = reinterpret_cast<int*>(smem_join);
+  float* buf = reinterpret_cast<float*>(smem_join);
+  int* cum = reinterpret_cast<int*>(smem_join + Lay::buf);
   const int g = p.H / p.HK, blocks = (g + HB - 1) / HB, items = p.HK * blocks;
   tile_line<Lay::TILE>(p, items, cum, scratch);
+  // The line depends on lens alone; the parts are there once the first kernel
+  // has ended.  Every block waits, so that this kernel does not end before it.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long total = cum[p.B];
   const int n = static_cast<int>(min(static_cast<long long>(grid), total));
   const int c = blockIdx.x + 1;
   if (c >= n) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int team = warp / Lay::WPT, member = warp % Lay::WPT;
   const int cut = static_cast<int>(stretch_start(total, c, n));
   const int before = static_cast<int>(stretch_start(total, c - 1, n));
   Cursor cur;
-  cur.seek(cum, p.B, items, cut);
+  cur.seek(p, cum, items, cut);
   const int start = cut - cur.tile, end = start + cur.ntiles;
   if (start == cut || start < before) return;  // no item is cut here, or an earlier cut has it
-  if (warp >= Lay::WPT) return;
-  constexpr int image = 32 * (Lay::NREG + 4 * MAPS);
   State<MAPS, Lay::MT> st;
   st.clear();
-  st.join(p.part + (2ll * (c - 1) + 1) * Lay::slot_floats + warp * image, lane);
-  for (int k = c; k < n && stretch_start(total, k, n) < end; ++k)
-    st.join(p.part + 2ll * k * Lay::slot_floats + warp * image, lane);
+  // part 0 ends stretch c - 1, part j > 0 begins stretch c - 1 + j
+  for (int j = team; j == 0 || (c - 1 + j < n && stretch_start(total, c - 1 + j, n) < end); j += Lay::TEAMS) {
+    const long long slot = 2ll * (c - 1 + j) + (j == 0 ? 1 : 0);
+    st.join(p.part + slot * Lay::slot_floats + member * Lay::image, lane);
+  }
+  join_warps<Lay>(st, buf, warp, lane);
+  if (team != 0) return;
   const int hk = cur.item / blocks, first = (cur.item % blocks) * HB;
-  st.template finish<F16>(p, cur.b, hk * g + first, min(HB, g - first), warp * Lay::DVW, lane);
+  st.template finish<F16>(p, cur.b, hk * g + first, min(HB, g - first), member * Lay::DVW, lane);
 }
 
 template <int D, int DV, int MAPS, bool F16>
@@ -524,9 +546,19 @@ cudaError_t launch_t(const PagedParams& p, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   kern<<<num_sms, NW * 32, smem, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  streamkl_paged_join_kernel<D, DV, MAPS, F16>
-      <<<num_sms - 1, NW * 32, (p.B + 1) * 4, stream>>>(p, num_sms);
-  return cudaGetLastError();
+  // The join's blocks start while the first kernel still runs and wait for it.
+  auto join = streamkl_paged_join_kernel<D, DV, MAPS, F16>;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms - 1);
+  cfg.blockDim = dim3(NW * 32);
+  cfg.dynamicSmemBytes = Lay::buf + (p.B + 1) * 4;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join, p, num_sms);
 }
 
 template <int MAPS, bool F16>

@@ -8,6 +8,9 @@ softmax map, ``paged_write`` puts new tokens' rows into the caches.
 
 As in ``binding``, this is argument marshalling only: tensors are checked for dtype, device, shape and
 layout, and every step of the computation runs in the library's kernels on the current stream.
+The checks of shapes, types and layouts are a function of these alone; their results (and the
+problem's C structs without pointers) are kept by them, since for one token's step they would take
+longer than the kernels.
 Tensors are bf16 or fp16 (one type for all of a call), with contiguous features; the other axes may
 have any positive strides that are multiples of 8 elements, so a projection's [B, N, H, d] output
 passes as ``.transpose(1, 2)`` without a copy.
@@ -15,10 +18,12 @@ passes as ``.transpose(1, 2)`` without a copy.
 from __future__ import annotations
 
 import ctypes
+import functools
+from collections import namedtuple
 
 import torch
 
-from .binding import EINVAL, OK, StreamKLError, _lib, _stream, _vp
+from .binding import EINVAL, OK, StreamKLError, _lib, _vp
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
@@ -39,123 +44,229 @@ class PagedProblem(ctypes.Structure):
                                                                           ("s2", ctypes.c_float)]
 
 
-_tp = ctypes.POINTER(_Tensor)
-_dp = ctypes.POINTER(DiffProblem)
-_gp = ctypes.POINTER(PagedProblem)
-_lib.streamkl_diff_fwd.argtypes = [_dp] + [_tp] * 6 + [_vp] * 2 + [_tp] * 2 + [_vp] * 3
+# Pointers to structs are passed as addresses.
+_sz = ctypes.c_size_t
+_lib.streamkl_diff_fwd.argtypes = [_vp] * 14
 _lib.streamkl_diff_fwd.restype = ctypes.c_int
-_lib.streamkl_diff_bwd_workspace_size.argtypes = [_dp]
-_lib.streamkl_diff_bwd_workspace_size.restype = ctypes.c_size_t
-_lib.streamkl_diff_bwd.argtypes = [_dp] + [_tp] * 9 + [_vp] * 4 + [_tp] * 5 + [_vp] * 2 + [ctypes.c_size_t, _vp]
+_lib.streamkl_diff_bwd_workspace_size.argtypes = [_vp]
+_lib.streamkl_diff_bwd_workspace_size.restype = _sz
+_lib.streamkl_diff_bwd.argtypes = [_vp] * 21 + [_sz, _vp]
 _lib.streamkl_diff_bwd.restype = ctypes.c_int
-_lib.streamkl_paged_workspace_size.argtypes = [_gp, ctypes.c_int]
-_lib.streamkl_paged_workspace_size.restype = ctypes.c_size_t
-_lib.streamkl_paged_attn.argtypes = [_gp] + [_tp] * 6 + [_vp, ctypes.c_int64, _vp, _tp, _vp, ctypes.c_size_t, _vp]
+_lib.streamkl_paged_workspace_size.argtypes = [_vp, ctypes.c_int]
+_lib.streamkl_paged_workspace_size.restype = _sz
+_lib.streamkl_paged_attn.argtypes = [_vp] * 8 + [ctypes.c_int64] + [_vp] * 3 + [_sz, _vp]
 _lib.streamkl_paged_attn.restype = ctypes.c_int
-_lib.streamkl_paged_write.argtypes = [ctypes.c_int, _tp, _tp, ctypes.POINTER(ctypes.c_int), _vp] + \
-    [ctypes.c_int] * 5 + [_vp]
+_lib.streamkl_paged_write.argtypes = [ctypes.c_int] + [_vp] * 4 + [ctypes.c_int] * 5 + [_vp]
 _lib.streamkl_paged_write.restype = ctypes.c_int
 
+# The current stream's handle, without a Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-def _ptr(t):
-    return _vp(t.data_ptr()) if t is not None else None
-
-
-def _layout_ok(t) -> bool:
-    """Contiguous features, 16-byte aligned, outer strides positive multiples of 8 elements."""
-    return (t.data_ptr() % 16 == 0 and (t.shape[-1] == 1 or t.stride(-1) == 1)
-            and all(n == 1 or (s > 0 and s % 8 == 0) for n, s in zip(t.shape[:-1], t.stride()[:-1])))
+# What the checks look at.
+_Meta = namedtuple("_Meta", "shape stride dtype device")
 
 
-def _check(name, t, shape, like, what):
+def _key(t):
+    """What a check of t depends on, as it comes; None for None."""
+    if t is None:
+        return None
+    try:
+        return t.shape, t.stride(), t.dtype, t.device
+    except AttributeError:
+        raise ValueError("operands must be tensors") from None
+
+
+def _meta(t):
+    """The same with names."""
+    return _Meta(*_key(t)) if t is not None else None
+
+
+def _planned(plan):
+    """A plan class as a function of keys: each key becomes a _Meta, the result is kept."""
+    def named(k):
+        if isinstance(k, tuple):
+            return _Meta(*k) if len(k) == 4 and isinstance(k[2], torch.dtype) else tuple(map(named, k))
+        return k
+    return functools.lru_cache(maxsize=512)(lambda *keys: plan(*map(named, keys)))
+
+
+def _contiguous(m) -> bool:
+    want = 1
+    for n, s in zip(reversed(m.shape), reversed(m.stride)):
+        if n != 1 and s != want and 0 not in m.shape:
+            return False
+        want *= n
+    return True
+
+
+def _layout_ok(m) -> bool:
+    """Contiguous features, outer strides positive multiples of 8 elements."""
+    return (m.shape[-1] == 1 or m.stride[-1] == 1) and \
+        all(n == 1 or (s > 0 and s % 8 == 0) for n, s in zip(m.shape[:-1], m.stride[:-1]))
+
+
+def _check(name, m, shape, like, what):
     """One 16-bit operand: its shape (None matches anything), type, device and layout."""
-    if not isinstance(t, torch.Tensor) or t.dim() != len(shape) or \
-            any(want is not None and want != got for want, got in zip(shape, t.shape)):
+    if m is None or len(m.shape) != len(shape) or \
+            any(want is not None and want != got for want, got in zip(shape, m.shape)):
         raise ValueError(f"{name} must be a tensor {what}")
-    if t.dtype not in _DTYPES or t.dtype != like.dtype:
+    if m.dtype not in _DTYPES or m.dtype != like.dtype:
         raise ValueError(f"{name} must be bf16 or fp16, the same type as the other operands")
-    if t.device != like.device:
+    if m.device != like.device:
         raise ValueError("tensors must be on one device")
-    if t.numel() and not _layout_ok(t):
-        raise ValueError(f"{name} must have contiguous features, 16-byte alignment and outer strides "
-                         "that are positive multiples of 8 elements")
+    if 0 not in m.shape and not _layout_ok(m):
+        raise ValueError(f"{name} must have contiguous features and outer strides that are positive "
+                         "multiples of 8 elements")
 
 
-def _check_out(name, t, ref_shape, like):
+def _check_out(name, m, shape, like):
     """A caller's output: as an operand, and no two of its elements in one place."""
-    _check(name, t, tuple(ref_shape), like, f"of shape {tuple(ref_shape)}")
+    _check(name, m, tuple(shape), like, f"of shape {tuple(shape)}")
     need = 1
-    for n, s in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1), key=lambda p: p[1]):
+    for s, n in sorted((s, n) for n, s in zip(m.shape, m.stride) if n > 1):
         if s < need:
             raise ValueError(f"{name} must not overlap itself")
         need = s * n
 
 
-def _check_cuda(t):
-    if not t.is_cuda:
+def _check_cuda(device):
+    if device.type != "cuda":
         raise ValueError("inputs must be CUDA tensors")
 
 
-def _check_lens(name, t, B, like):
-    if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.shape != (B,)
-                          or not t.is_contiguous() or t.device != like.device):
+def _check_lens(name, m, B, like):
+    if m is not None and (m.dtype != torch.int32 or tuple(m.shape) != (B,) or not _contiguous(m)
+                          or m.device != like.device):
         raise ValueError(f"{name} must be a contiguous int32 tensor [B] on the inputs' device")
 
 
-def _check_lam(lam, extents, like):
-    """lam as a tensor with one axis per extent, broadcast axes of stride 0."""
-    names = "[H], [B, H, N]" if len(extents) == 3 else "[H], [B, H]"
-    if not isinstance(lam, torch.Tensor) or lam.dtype not in (like.dtype, torch.float32) or \
-            lam.device != like.device:
+def _check_rows(name, m, shape, like):
+    if m is None or m.dtype != torch.float32 or tuple(m.shape) != tuple(shape) or not _contiguous(m) \
+            or m.device != like.device:
+        raise ValueError(f"{name} must be a contiguous fp32 tensor [B, H, NQ] on the inputs' device")
+
+
+def _check_same_strides(O, O2):
+    if 0 not in O.shape and any(n > 1 and a != b for n, a, b in zip(O.shape, O.stride, O2.stride)):
+        raise ValueError("O and O2 must have the same strides")
+
+
+def _lam_strides(m, extents, like):
+    """Element strides of lam along the extents, 0 where it is broadcast."""
+    if m is None or m.dtype not in (like.dtype, torch.float32) or m.device != like.device:
         raise ValueError("lam must be a tensor of the inputs' type or fp32 on their device")
-    if lam.dim() == 0:
-        shape = (1,) * len(extents)
-    elif lam.dim() == 1:
-        shape = (1, lam.shape[0]) + (1,) * (len(extents) - 2)
-    else:
-        shape = tuple(lam.shape)
+    shape, stride = tuple(m.shape), tuple(m.stride)
+    if len(shape) == 0:
+        shape, stride = (1,) * len(extents), (0,) * len(extents)
+    elif len(shape) == 1:
+        shape, stride = (1, *shape) + (1,) * (len(extents) - 2), (0, *stride) + (0,) * (len(extents) - 2)
     if len(shape) != len(extents) or any(n not in (1, e) for n, e in zip(shape, extents)):
-        raise ValueError(f"lam must be a scalar or {names} (extents of 1 broadcast)")
-    view = lam.reshape(shape)
-    if any(n > 1 and s <= 0 for n, s in zip(view.shape, view.stride())):
-        view = view.contiguous()
-    return view
+        raise ValueError("lam must be a scalar, [H], or one weight per " +
+                         ("[B, H, NQ]" if len(extents) == 3 else "[B, H]") + " (extents of 1 broadcast)")
+    return (*(s if n > 1 else 0 for n, s in zip(shape, stride)), 0)[:3]
 
 
-def _tensor(t):
-    """The streamkl_tensor of [.., .., .., width] (or, with fewer axes, of the leading ones)."""
-    if t is None:
-        return None
-    st = t.stride()
-    return ctypes.byref(_Tensor(t.data_ptr(), *(st[k] if k < t.dim() - 1 else 0 for k in range(3))))
-
-
-def _lam_tensor(view):
-    st = [s if n > 1 else 0 for n, s in zip(view.shape, view.stride())]
-    return ctypes.byref(_Tensor(view.data_ptr(), *(st + [0])[:3]))
+def _lam(lam):
+    """lam itself, or a copy where an axis of it was expanded: each element then has a place."""
+    if not isinstance(lam, torch.Tensor) or lam.is_contiguous():
+        return lam
+    return lam.contiguous() if any(n > 1 and s <= 0 for n, s in zip(lam.shape, lam.stride())) else lam
 
 
 def _scale(s):
     return float(s) if s is not None else 0.0
 
 
-def _check_diff(Q1, K1, Q2, K2, V, lam, q_lens, k_lens):
-    if not isinstance(Q1, torch.Tensor) or Q1.dim() != 4:
-        raise ValueError("Q1 must be a tensor [B, H, NQ, d]")
-    B, H, NQ, d = Q1.shape
-    _check("Q1", Q1, (B, H, NQ, d), Q1, "[B, H, NQ, d]")
-    _check("Q2", Q2, (B, H, NQ, d), Q1, "[B, H, NQ, d], as Q1")
-    _check("K1", K1, (B, None, None, d), Q1, "[B, HK, NK, d]")
-    HK, NK = K1.shape[1:3]
-    _check("K2", K2, (B, HK, NK, d), Q1, "[B, HK, NK, d], as K1")
-    _check("V", V, (B, HK, NK, None), Q1, "[B, HK, NK, dv]")
-    if (HK == 0) != (H == 0) or (HK and H % HK != 0):
-        raise ValueError("the key heads must divide the query heads")
-    _check_lens("q_lens", q_lens, B, Q1)
-    _check_lens("k_lens", k_lens, B, Q1)
-    view = _check_lam(lam, (B, H, NQ), Q1)
-    _check_cuda(Q1)
-    return (B, H, HK, NQ, NK, d, V.shape[3]), view
+class _Structs:
+    """streamkl_tensor structs without their pointers; ``at`` puts the pointers in, in a new copy, and
+    gives the addresses to pass.  Entries of None stay NULL."""
+
+    def __init__(self, strides):
+        words = []
+        for st in strides:
+            words += [0, *(st if st is not None else (0, 0, 0))]
+        self.type = ctypes.c_uint64 * len(words)
+        self.template = bytes(self.type(*(w % 2 ** 64 for w in words)))
+
+    def at(self, pointers):
+        block = self.type.from_buffer_copy(self.template)
+        base = ctypes.addressof(block)
+        out = []
+        for k, p in enumerate(pointers):
+            if p is None:
+                out.append(None)
+            else:
+                block[4 * k] = p
+                out.append(base + 32 * k)
+        return block, out
+
+
+def _outer(m):
+    """The three outer strides of an operand, or of a row operand with fewer axes the leading ones."""
+    return (*m.stride[:-1], 0, 0)[:3]
+
+
+def _order(m):
+    """The outer axes from the slowest to the fastest in memory, and where each one went."""
+    order = sorted(range(len(m.shape) - 1), key=lambda k: (-m.stride[k], k))
+    back = [0] * len(m.shape)
+    for place, k in enumerate(order):
+        back[k] = place
+    back[-1] = len(m.shape) - 1
+    return tuple(order), tuple(back)
+
+
+@functools.lru_cache(maxsize=512)
+def _like_shape(shape, stride, width):
+    order, back = _order(_Meta(shape, stride, None, None))
+    return [*(shape[k] for k in order), width], back if order != tuple(range(len(order))) else None
+
+
+def _like(m, width):
+    """An empty tensor of m's shape but `width` features, its axes in m's memory order."""
+    shape, back = _like_shape(m.shape, m.stride, width)
+    out = torch.empty(shape, dtype=m.dtype, device=m.device)
+    return out if back is None else out.permute(back)
+
+
+def _pointers(*tensors):
+    """Data pointers, None for None; operands start on 16 bytes."""
+    out = [None if t is None else t.data_ptr() for t in tensors]
+    low = 0
+    for p in out:
+        low |= p or 0
+    if low & 15:
+        raise ValueError("operands must be 16-byte aligned")
+    return out
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _run(fn, where, device, *args):
+    """Calls the library on the current stream of `device`, that device current."""
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _raw_stream(device.index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _raw_stream(device.index))
+    if st != OK:
+        raise StreamKLError(st, where)
+
+
+def _workspace(ws, need, device):
+    """The caller's workspace, or one from the caching allocator: (tensor, pointer, bytes)."""
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        return ws, ws.data_ptr(), need
+    if not isinstance(ws, torch.Tensor) or ws.device != device or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    have = ws.numel() * ws.element_size()
+    if have < need:
+        raise ValueError("workspace too small")
+    return ws, ws.data_ptr(), have
 
 
 def diff_problem(B, H, HK, NQ, NK, d, dv, causal=False, s1=None, s2=None, dtype=torch.bfloat16,
@@ -164,15 +275,48 @@ def diff_problem(B, H, HK, NQ, NK, d, dv, causal=False, s1=None, s2=None, dtype=
                        _scale(s1), _scale(s2))
 
 
-def _like(t, width):
-    """An empty tensor of t's shape but `width` features, its axes in t's memory order."""
-    order = sorted(range(t.dim() - 1), key=lambda k: (-t.stride(k), k))
-    out = torch.empty([t.shape[k] for k in order] + [width], dtype=t.dtype, device=t.device)
-    back = [0] * t.dim()
-    for place, k in enumerate(order):
-        back[k] = place
-    back[-1] = t.dim() - 1
-    return out.permute(back)
+class _DiffPlan:
+    """One problem's checked dimensions and C structs."""
+
+    def __init__(self, Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2):
+        if Q1 is None or len(Q1.shape) != 4:
+            raise ValueError("Q1 must be a tensor [B, H, NQ, d]")
+        B, H, NQ, d = Q1.shape
+        _check("Q1", Q1, (B, H, NQ, d), Q1, "[B, H, NQ, d]")
+        _check("Q2", Q2, (B, H, NQ, d), Q1, "[B, H, NQ, d], as Q1")
+        _check("K1", K1, (B, None, None, d), Q1, "[B, HK, NK, d]")
+        HK, NK = K1.shape[1:3]
+        _check("K2", K2, (B, HK, NK, d), Q1, "[B, HK, NK, d], as K1")
+        _check("V", V, (B, HK, NK, None), Q1, "[B, HK, NK, dv]")
+        if (HK == 0) != (H == 0) or (HK and H % HK != 0):
+            raise ValueError("the key heads must divide the query heads")
+        _check_lens("q_lens", q_lens, B, Q1)
+        _check_lens("k_lens", k_lens, B, Q1)
+        lam_strides = _lam_strides(lam, (B, H, NQ), Q1)
+        _check_cuda(Q1.device)
+        dv = V.shape[3]
+        self.device, self.dtype = Q1.device, Q1.dtype
+        self.rows, self.out, self.q = (B, H, NQ), (B, H, NQ, dv), Q1
+        self.empty = 0 in self.out or HK == 0
+        self.mO = None  # an output's layout, once there has been one
+        self.no_keys = NK == 0
+        self.prob = diff_problem(B, H, HK, NQ, NK, d, dv, causal, s1, s2, Q1.dtype, lam.dtype == torch.float32)
+        self.prob_at = ctypes.addressof(self.prob)
+        self.inputs = [*map(_outer, (Q1, K1, Q2, K2, V)), lam_strides]
+        self.ws_bytes = max(256, int(_lib.streamkl_diff_bwd_workspace_size(self.prob_at)))
+
+
+_diff_plan = _planned(_DiffPlan)
+
+
+def _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2):
+    return _diff_plan(_key(Q1), _key(K1), _key(Q2), _key(K2), _key(V), _key(lam), _key(q_lens),
+                      _key(k_lens), bool(causal), s1, s2)
+
+
+@functools.lru_cache(maxsize=512)
+def _fwd_structs(plan, O, O2):
+    return _Structs([*plan.inputs, _outer(O), _outer(O2) if O2 is not None else None])
 
 
 def diff_attn_fwd(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens=None, k_lens=None,
@@ -187,52 +331,55 @@ def diff_attn_fwd(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens
     self-attention batch passes both.  Rows that see no key give O = 0 and LSE = -inf.
     O2 = P2 V and the LSEs are what ``diff_attn_bwd`` needs; ``save=False`` leaves them out (None).
     ``out`` may hold a preallocated O, and with ``save`` O2, LSE1, LSE2."""
-    (B, H, HK, NQ, NK, d, dv), lv = _check_diff(Q1, K1, Q2, K2, V, lam, q_lens, k_lens)
+    lam = _lam(lam)
+    plan = _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2)
     if out is None:
-        O = _like(Q1, dv)
+        O = _like(plan.q, plan.out[3])
+        if plan.mO is None:
+            plan.mO = _meta(O)
         O2 = torch.empty_like(O) if save else None
-        LSE1, LSE2 = (torch.empty((B, H, NQ), dtype=torch.float32, device=Q1.device)
+        LSE1, LSE2 = (torch.empty(plan.rows, dtype=torch.float32, device=plan.device)
                       if save else None for _ in range(2))
+        mO, mO2 = plan.mO, plan.mO if save else None
     else:
-        O, O2, LSE1, LSE2 = tuple(out) if save else (*tuple(out)[:1], None, None, None)
-        for name, t in (("O", O), ("O2", O2)):
-            if t is not None or name == "O" or save:
-                _check_out(name, t, (B, H, NQ, dv), Q1)
-        if save and O.numel() and any(n > 1 and a != b for n, a, b in zip(O.shape, O.stride(), O2.stride())):
-            raise ValueError("O and O2 must have the same strides")
+        out = tuple(out)
+        if len(out) != 4:
+            raise ValueError("out must hold four entries: O, O2, LSE1, LSE2")
+        O, O2, LSE1, LSE2 = out if save else (out[0], None, None, None)
+        mO, mO2 = _meta(O), _meta(O2)
+        _check_out("O", mO, plan.out, plan.q)
         if save:
-            _check_rows((("LSE1", LSE1), ("LSE2", LSE2)), (B, H, NQ), Q1)
-    if O.numel() == 0:
-        return O, O2, LSE1, LSE2
-    if NK == 0:
-        for t in (O, O2):
+            _check_out("O2", mO2, plan.out, plan.q)
+            _check_same_strides(mO, mO2)
+            _check_rows("LSE1", _meta(LSE1), plan.rows, plan.q)
+            _check_rows("LSE2", _meta(LSE2), plan.rows, plan.q)
+    if plan.empty or plan.no_keys:
+        for t, v in ((O, 0.0), (O2, 0.0), (LSE1, -float("inf")), (LSE2, -float("inf"))):
             if t is not None:
-                t.zero_()
-        for t in (LSE1, LSE2):
-            if t is not None:
-                t.fill_(-float("inf"))
+                t.fill_(v)
         return O, O2, LSE1, LSE2
-    prob = diff_problem(B, H, HK, NQ, NK, d, dv, causal, s1, s2, Q1.dtype, lv.dtype == torch.float32)
-    with torch.cuda.device(Q1.device):
-        st = _lib.streamkl_diff_fwd(ctypes.byref(prob), *map(_tensor, (Q1, K1, Q2, K2, V)), _lam_tensor(lv),
-                                    _ptr(q_lens), _ptr(k_lens), _tensor(O), _tensor(O2), _ptr(LSE1),
-                                    _ptr(LSE2), _stream(Q1.device))
-    if st != OK:
-        raise StreamKLError(st, "streamkl_diff_fwd")
+    p = _pointers(Q1, K1, Q2, K2, V, O, O2)
+    block, at = _fwd_structs(plan, mO, mO2).at([*p[:5], lam.data_ptr(), *p[5:]])
+    _run(_lib.streamkl_diff_fwd, "streamkl_diff_fwd", plan.device, plan.prob_at, *at[:6], _ptr(q_lens),
+         _ptr(k_lens), *at[6:], _ptr(LSE1), _ptr(LSE2))
     return O, O2, LSE1, LSE2
-
-
-def _check_rows(named, shape, like):
-    for name, t in named:
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.shape != shape \
-                or not t.is_contiguous() or t.device != like.device:
-            raise ValueError(f"{name} must be a contiguous fp32 tensor [B, H, NQ] on the inputs' device")
 
 
 def diff_attn_workspace_size(B, H, HK, NQ, NK, d, dv, causal=False) -> int:
     """Bytes of the workspace of ``diff_attn_bwd`` (0 on a bad problem)."""
     prob = diff_problem(B, H, HK, NQ, NK, d, dv, causal)
-    return int(_lib.streamkl_diff_bwd_workspace_size(ctypes.byref(prob)))
+    return int(_lib.streamkl_diff_bwd_workspace_size(ctypes.addressof(prob)))
+
+
+@functools.lru_cache(maxsize=512)
+def _bwd_structs(plan, dO, O, O2, LSE1, LSE2, grads):
+    for name, m in (("dO", dO), ("O", O), ("O2", O2)):
+        _check(name, m, plan.out, plan.q, "[B, H, NQ, dv]")
+    _check_same_strides(O, O2)
+    _check_rows("LSE1", LSE1, plan.rows, plan.q)
+    _check_rows("LSE2", LSE2, plan.rows, plan.q)
+    return _Structs([_outer(dO), *plan.inputs, _outer(O), _outer(O2),
+                     *(_outer(m) if m is not None else None for m in grads)])
 
 
 def diff_attn_bwd(dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, causal=False, s1=None, s2=None,
@@ -246,20 +393,16 @@ def diff_attn_bwd(dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, causal=False, s
     16-bit operands allow, and fp16 training wants the usual loss scale.
     ``out`` may pass preallocated gradients (None entries are skipped), ``workspace`` a device buffer
     of at least ``diff_attn_workspace_size`` bytes, 256-byte aligned."""
-    (B, H, HK, NQ, NK, d, dv), lv = _check_diff(Q1, K1, Q2, K2, V, lam, q_lens, k_lens)
-    for name, t in (("dO", dO), ("O", O), ("O2", O2)):
-        _check(name, t, (B, H, NQ, dv), Q1, "[B, H, NQ, dv]")
-    if O.numel() and any(n > 1 and a != b for n, a, b in zip(O.shape, O.stride(), O2.stride())):
-        raise ValueError("O and O2 must have the same strides")
-    _check_rows((("LSE1", LSE1), ("LSE2", LSE2)), (B, H, NQ), Q1)
-    inputs = (Q1, K1, Q2, K2, V, lam)
+    shape_lam, lam = lam, _lam(lam)
+    plan = _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2)
+    inputs = (Q1, K1, Q2, K2, V)
     if out is not None:
         if len(out) != 6:
             raise ValueError("out must hold six entries: dQ1, dK1, dQ2, dK2, dV, dlam (None skips one)")
         outs = list(out)
         for name, o, t in zip(("dQ1", "dK1", "dQ2", "dK2", "dV"), outs, inputs):
             if o is not None:
-                _check_out(name, o, t.shape, Q1)
+                _check_out(name, _meta(o), t.shape, plan.q)
         o = outs[5]
         if o is not None and (not isinstance(o, torch.Tensor) or o.shape != lam.shape or o.dtype != lam.dtype
                               or not o.is_contiguous() or o.device != lam.device):
@@ -267,37 +410,23 @@ def diff_attn_bwd(dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, causal=False, s
     else:
         if len(need) != 6:
             raise ValueError("need must hold six entries: dQ1, dK1, dQ2, dK2, dV, dlam")
-        outs = [_like(t, t.shape[-1]) if want else None for t, want in zip(inputs[:5], need)]
-        outs.append(torch.empty(lam.shape, dtype=lam.dtype, device=lam.device) if need[5] else None)
+        outs = [_like(_meta(t), t.shape[-1]) if want else None for t, want in zip(inputs, need)]
+        outs.append(torch.empty(shape_lam.shape, dtype=lam.dtype, device=lam.device) if need[5] else None)
     if all(o is None for o in outs):
         raise ValueError("no gradient is asked for")
-    if Q1.numel() == 0 or K1.numel() == 0:
+    structs = _bwd_structs(plan, _meta(dO), _meta(O), _meta(O2), _meta(LSE1), _meta(LSE2),
+                           tuple(map(_meta, outs[:5])))
+    if plan.empty or plan.no_keys:
         for o in outs:
             if o is not None:
                 o.zero_()
         return tuple(outs)
-    prob = diff_problem(B, H, HK, NQ, NK, d, dv, causal, s1, s2, Q1.dtype, lv.dtype == torch.float32)
-    ws_bytes = int(_lib.streamkl_diff_bwd_workspace_size(ctypes.byref(prob)))
-    workspace = _workspace(workspace, ws_bytes, Q1)
-    with torch.cuda.device(Q1.device):
-        st = _lib.streamkl_diff_bwd(ctypes.byref(prob), _tensor(dO), *map(_tensor, (Q1, K1, Q2, K2, V)),
-                                    _lam_tensor(lv), _tensor(O), _tensor(O2), _ptr(LSE1), _ptr(LSE2),
-                                    _ptr(q_lens), _ptr(k_lens), *map(_tensor, outs[:5]), _ptr(outs[5]),
-                                    *workspace, _stream(Q1.device))
-    if st != OK:
-        raise StreamKLError(st, "streamkl_diff_bwd")
+    p = _pointers(dO, *inputs, O, O2, *outs[:5])
+    block, at = structs.at([*p[:6], lam.data_ptr(), *p[6:]])
+    ws, ws_at, ws_bytes = _workspace(workspace, plan.ws_bytes, plan.device)
+    _run(_lib.streamkl_diff_bwd, "streamkl_diff_bwd", plan.device, plan.prob_at, *at[:9], _ptr(LSE1),
+         _ptr(LSE2), _ptr(q_lens), _ptr(k_lens), *at[9:], _ptr(outs[5]), ws_at, ws_bytes)
     return tuple(outs)
-
-
-def _workspace(ws, need, like):
-    """(pointer, bytes) of the caller's workspace, or of one from the caching allocator."""
-    if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=like.device)
-    elif not isinstance(ws, torch.Tensor) or ws.device != like.device or not ws.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    elif ws.numel() * ws.element_size() < need:
-        raise ValueError("workspace too small")
-    return _vp(ws.data_ptr()), ctypes.c_size_t(ws.numel() * ws.element_size())
 
 
 class _DiffAttnFunction(torch.autograd.Function):
@@ -315,8 +444,8 @@ class _DiffAttnFunction(torch.autograd.Function):
         need = tuple(bool(x) for x in ctx.needs_input_grad[:6])
         if not any(need):
             return (None,) * 11
-        if not _layout_ok(dO):  # an expanded or sliced upstream gradient
-            dO = dO.contiguous()
+        if dO.data_ptr() % 16 or not _layout_ok(_meta(dO)):  # an expanded or sliced upstream gradient
+            dO = dO.clone(memory_format=torch.contiguous_format)
         return (*diff_attn_bwd(dO, *state, *ctx.cfg, q_lens, k_lens, need=need), *(None,) * 5)
 
 
@@ -331,52 +460,72 @@ def diff_attn(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens=Non
     return diff_attn_fwd(Q1, K1, Q2, K2, V, lam, causal, s1, s2, q_lens, k_lens, save=False)[0]
 
 
-def _paged(Q1, K1, Q2, K2, V, lam, table, lens, s1, s2, workspace, out, where):
-    if not isinstance(Q1, torch.Tensor) or Q1.dim() != 3:
-        raise ValueError("the query must be a tensor [B, H, d]")
-    B, H, d = Q1.shape
-    _check("Q1" if Q2 is not None else "Q", Q1, (B, H, d), Q1, "[B, H, d]")
-    _check("K1" if Q2 is not None else "K", K1, (None, None, None, d), Q1, "[pages, page_size, HK, d]")
-    pages, page_size, HK, _ = K1.shape
-    _check("V", V, (pages, page_size, HK, None), Q1, "[pages, page_size, HK, dv]")
-    if HK == 0 or H % HK != 0:
-        raise ValueError("the key heads must divide the query heads")
-    lv = None
-    if Q2 is not None:
-        _check("Q2", Q2, (B, H, d), Q1, "[B, H, d], as Q1")
-        _check("K2", K2, (pages, page_size, HK, d), Q1, "[pages, page_size, HK, d], as K1")
-        lv = _check_lam(lam, (B, H), Q1)
-    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2 or \
-            table.shape[0] != B or table.device != Q1.device or (table.shape[1] > 1 and table.stride(1) != 1) \
-            or (B > 1 and table.stride(0) < table.shape[1]):
-        raise ValueError("table must be an int32 tensor [B, pages of a sequence] on the inputs' device, "
-                         "its rows contiguous and apart")
-    if lens is None:
-        raise ValueError("lens must be a contiguous int32 tensor [B] on the inputs' device")
-    _check_lens("lens", lens, B, Q1)
-    dv = V.shape[3]
+class _PagedPlan:
+    """One paged problem's checked dimensions and C structs."""
+
+    def __init__(self, Q1, K1, Q2, K2, V, lam, table, lens, out, s1, s2):
+        if Q1 is None or len(Q1.shape) != 3:
+            raise ValueError("the query must be a tensor [B, H, d]")
+        B, H, d = Q1.shape
+        two = Q2 is not None
+        _check("Q1" if two else "Q", Q1, (B, H, d), Q1, "[B, H, d]")
+        _check("K1" if two else "K", K1, (None, None, None, d), Q1, "[pages, page_size, HK, d]")
+        pages, page_size, HK, _ = K1.shape
+        _check("V", V, (pages, page_size, HK, None), Q1, "[pages, page_size, HK, dv]")
+        if HK == 0 or H % HK != 0:
+            raise ValueError("the key heads must divide the query heads")
+        if two:
+            _check("Q2", Q2, (B, H, d), Q1, "[B, H, d], as Q1")
+            _check("K2", K2, (pages, page_size, HK, d), Q1, "[pages, page_size, HK, d], as K1")
+        lam_strides = _lam_strides(lam, (B, H), Q1) if two else None
+        if table is None or table.dtype != torch.int32 or len(table.shape) != 2 or table.shape[0] != B or \
+                table.device != Q1.device or (table.shape[1] > 1 and table.stride[1] != 1) or \
+                (B > 1 and table.stride[0] < table.shape[1]):
+            raise ValueError("table must be an int32 tensor [B, pages of a sequence] on the inputs' device, "
+                             "its rows contiguous and apart")
+        if lens is None:
+            raise ValueError("lens must be a contiguous int32 tensor [B] on the inputs' device")
+        _check_lens("lens", lens, B, Q1)
+        dv = V.shape[3]
+        self.out, self.dtype, self.device = (B, H, dv), Q1.dtype, Q1.device
+        if out is not None:
+            _check_out("out", out, self.out, Q1)
+        _check_cuda(Q1.device)
+        self.empty = 0 in self.out
+        self.no_keys = pages == 0 or page_size == 0 or table.shape[1] == 0
+        self.table_stride = table.stride[0]
+        self.prob = PagedProblem(B, H, HK, d, dv, _DTYPES[Q1.dtype], int(two and lam.dtype == torch.float32),
+                                 pages, page_size, table.shape[1], _scale(s1), _scale(s2))
+        self.prob_at = ctypes.addressof(self.prob)
+
+        def cache(m):  # page, head, row
+            return (m.stride[0], m.stride[2], m.stride[1]) if m is not None else None
+
+        self.structs = _Structs([_outer(Q1), cache(K1), _outer(Q2) if two else None, cache(K2), cache(V),
+                                 lam_strides, _outer(out) if out is not None else (H * dv, dv, 0)])
+        self.ws_bytes = 0
+        if not (self.empty or self.no_keys):
+            with torch.cuda.device(Q1.device):
+                # 0 for a problem that the call itself refuses
+                self.ws_bytes = max(256, int(_lib.streamkl_paged_workspace_size(self.prob_at, 2 if two else 1)))
+
+
+_paged_plan = _planned(_PagedPlan)
+
+
+def _paged(Q1, K1, Q2, K2, V, lam, table, lens, s1, s2, workspace, out):
+    lam = _lam(lam)
+    plan = _paged_plan(_key(Q1), _key(K1), _key(Q2), _key(K2), _key(V), _key(lam), _key(table),
+                       _key(lens), _key(out), s1, s2)
     if out is None:
-        out = torch.empty((B, H, dv), dtype=Q1.dtype, device=Q1.device)
-    else:
-        _check_out("out", out, (B, H, dv), Q1)
-    _check_cuda(Q1)
-    if out.numel() == 0:
-        return out
-    if K1.numel() == 0 or V.numel() == 0 or table.shape[1] == 0:
+        out = torch.empty(plan.out, dtype=plan.dtype, device=plan.device)
+    if plan.empty or plan.no_keys:
         return out.zero_()
-    prob = PagedProblem(B, H, HK, d, dv, _DTYPES[Q1.dtype], int(lv is not None and lv.dtype == torch.float32),
-                        pages, page_size, table.shape[1], _scale(s1), _scale(s2))
-    with torch.cuda.device(Q1.device):
-        need = int(_lib.streamkl_paged_workspace_size(ctypes.byref(prob), 1 if Q2 is None else 2))
-        # a cache's axes in the order that the library names them: page, head, row
-        caches = [t.transpose(1, 2) if t is not None else None for t in (K1, K2, V)]
-        st = _lib.streamkl_paged_attn(
-            ctypes.byref(prob), _tensor(Q1), _tensor(caches[0]), _tensor(Q2), _tensor(caches[1]),
-            _tensor(caches[2]), _lam_tensor(lv) if lv is not None else None, _ptr(table),
-            table.stride(0), _ptr(lens), _tensor(out), *_workspace(workspace, need, Q1),
-            _stream(Q1.device))
-    if st != OK:
-        raise StreamKLError(st, where)
+    p = _pointers(Q1, K1, Q2, K2, V, out)
+    block, at = plan.structs.at([*p[:5], _ptr(lam), p[5]])
+    ws, ws_at, ws_bytes = _workspace(workspace, plan.ws_bytes, plan.device)
+    _run(_lib.streamkl_paged_attn, "streamkl_paged_attn", plan.device, plan.prob_at, *at[:6],
+         table.data_ptr(), plan.table_stride, lens.data_ptr(), at[6], ws_at, ws_bytes)
     return out
 
 
@@ -391,7 +540,7 @@ def attn_paged(Q, K, V, table, lens, s=None, workspace=None, out=None):
     The work is split over the device by lens as they are when the kernel runs, so a captured call
     follows lengths that grow.  Results repeat bit for bit.  ``workspace`` may pass a device buffer
     of at least ``paged_workspace_size`` bytes, 256-byte aligned."""
-    return _paged(Q, K, None, None, V, None, table, lens, s, None, workspace, out, "streamkl_paged_attn")
+    return _paged(Q, K, None, None, V, None, table, lens, s, None, workspace, out)
 
 
 def diff_attn_paged(Q1, K1, Q2, K2, V, lam, table, lens, s1=None, s2=None, workspace=None, out=None):
@@ -399,17 +548,53 @@ def diff_attn_paged(Q1, K1, Q2, K2, V, lam, table, lens, s1=None, s2=None, works
     that share one table.  Arguments as in ``attn_paged``; lam is a scalar tensor, [H] or [B, H]."""
     if Q2 is None or K2 is None or lam is None:
         raise ValueError("Q2, K2 and lam are needed")
-    return _paged(Q1, K1, Q2, K2, V, lam, table, lens, s1, s2, workspace, out, "streamkl_paged_attn")
+    return _paged(Q1, K1, Q2, K2, V, lam, table, lens, s1, s2, workspace, out)
 
 
 def paged_workspace_size(dv, maps, device=None) -> int:
     """Bytes of the workspace of ``attn_paged`` (maps 1) or ``diff_attn_paged`` (maps 2) on a device."""
-    prob = PagedProblem(1, 1, 1, 64 if dv == 64 else 128 if dv == 256 else 64, dv, 0, 0, 1, 1, 1, 0.0, 0.0)
+    prob = PagedProblem(1, 1, 1, 128 if dv == 256 else 64, dv, 0, 0, 1, 1, 1, 0.0, 0.0)
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
-        n = int(_lib.streamkl_paged_workspace_size(ctypes.byref(prob), int(maps)))
+        n = int(_lib.streamkl_paged_workspace_size(ctypes.addressof(prob), int(maps)))
     if n == 0:
         raise StreamKLError(EINVAL, "streamkl_paged_workspace_size")
     return n
+
+
+class _WritePlan:
+    """One write's checked dimensions and C structs."""
+
+    def __init__(self, rows, caches, slots):
+        first = rows[0]
+        if first is None or len(first.shape) != 3:
+            raise ValueError("rows[0] must be a tensor [T, HK, width]")
+        T, HK = first.shape[:2]
+        for k, (r, c) in enumerate(zip(rows, caches)):
+            _check(f"rows[{k}]", r, (T, HK, None), first, "[T, HK, width]")
+            _check(f"caches[{k}]", c, (None, None, HK, r.shape[2]), first, "[pages, page_size, HK, width]")
+            _check_out(f"caches[{k}]", c, c.shape, first)
+            if c.shape[:2] != caches[0].shape[:2]:
+                raise ValueError("the caches must have the same pages and page size")
+            if r.shape[2] % 8 != 0:
+                raise ValueError("widths must be multiples of 8")
+        if slots is None or slots.dtype not in (torch.int32, torch.int64) or tuple(slots.shape) != (T,) or \
+                not _contiguous(slots) or slots.device != first.device:
+            raise ValueError("slots must be a contiguous int32 or int64 tensor [T] on the rows' device")
+        _check_cuda(first.device)
+        self.empty = any(0 in r.shape for r in rows)
+        if self.empty and not all(0 in r.shape for r in rows):
+            raise ValueError("rows must all be empty or none")
+        if not self.empty and 0 in caches[0].shape:
+            raise ValueError("there is no slot to write to")
+        self.device, self.n = first.device, len(rows)
+        self.structs = _Structs([(0, r.stride[1], r.stride[0]) for r in rows] +
+                                [(c.stride[0], c.stride[2], c.stride[1]) for c in caches])
+        self.widths = (ctypes.c_int * self.n)(*(r.shape[2] for r in rows))
+        self.widths_at = ctypes.addressof(self.widths)
+        self.tail = (int(slots.dtype == torch.int64), T, HK, *caches[0].shape[:2])
+
+
+_write_plan = _planned(_WritePlan)
 
 
 def paged_write(rows, caches, slots):
@@ -420,36 +605,12 @@ def paged_write(rows, caches, slots):
     (int32 or int64 [T]).  A negative slot is skipped, one past the cache is skipped and recorded for
     ``query_device_status``.  Slots must be distinct; the rest of the caches stays as it was."""
     rows, caches = tuple(rows), tuple(caches)
-    if not 1 <= len(rows) <= 4 or len(rows) != len(caches):
-        raise ValueError("rows and caches must be tuples of the same length, one to four")
-    first = rows[0]
-    if not isinstance(first, torch.Tensor) or first.dim() != 3:
-        raise ValueError("rows[0] must be a tensor [T, HK, width]")
-    T, HK = first.shape[:2]
-    for k, (r, c) in enumerate(zip(rows, caches)):
-        _check(f"rows[{k}]", r, (T, HK, None), first, "[T, HK, width]")
-        shape = (None, None, HK, r.shape[2])
-        _check(f"caches[{k}]", c, shape, first, "[pages, page_size, HK, width]")
-        _check_out(f"caches[{k}]", c, c.shape, first)
-        if c.shape[:2] != caches[0].shape[:2]:
-            raise ValueError("the caches must have the same pages and page size")
-        if r.shape[2] % 8 != 0:
-            raise ValueError("widths must be multiples of 8")
-    if not isinstance(slots, torch.Tensor) or slots.dtype not in (torch.int32, torch.int64) or \
-            slots.shape != (T,) or not slots.is_contiguous() or slots.device != first.device:
-        raise ValueError("slots must be a contiguous int32 or int64 tensor [T] on the rows' device")
-    _check_cuda(first)
-    if any(r.numel() == 0 for r in rows) or caches[0].numel() == 0:
-        if all(r.numel() == 0 for r in rows):
-            return
-        raise ValueError("there is no slot to write to")
     n = len(rows)
-    rt = (_Tensor * n)(*(_Tensor(r.data_ptr(), 0, r.stride(1), r.stride(0)) for r in rows))
-    ct = (_Tensor * n)(*(_Tensor(c.data_ptr(), c.stride(0), c.stride(2), c.stride(1)) for c in caches))
-    widths = (ctypes.c_int * n)(*(r.shape[2] for r in rows))
-    pages, page_size = caches[0].shape[:2]
-    with torch.cuda.device(first.device):
-        st = _lib.streamkl_paged_write(n, rt, ct, widths, _ptr(slots), int(slots.dtype == torch.int64), T, HK,
-                                       pages, page_size, _stream(first.device))
-    if st != OK:
-        raise StreamKLError(st, "streamkl_paged_write")
+    if not 1 <= n <= 4 or n != len(caches):
+        raise ValueError("rows and caches must be tuples of the same length, one to four")
+    plan = _write_plan(tuple(map(_key, rows)), tuple(map(_key, caches)), _key(slots))
+    if plan.empty:
+        return
+    block, at = plan.structs.at(_pointers(*rows, *caches))
+    _run(_lib.streamkl_paged_write, "streamkl_paged_write", plan.device, n, at[0], at[n], plan.widths_at,
+         slots.data_ptr(), *plan.tail)
