@@ -78,6 +78,7 @@ struct DiffPrepParams {
   const float* LSE1;
   const float* LSE2;
   float* rec;  // [B*H][NQpad/64][kDiffRec][64]
+  float* sums; // [B*H][NQpad/64]: D2 summed over the rows of a step
   int NQpad, dv, f16;
 };
 cudaError_t launch_diff_prep(const DiffPrepParams& p, int num_sms, cudaStream_t stream);
@@ -85,6 +86,7 @@ cudaError_t launch_diff_prep(const DiffPrepParams& p, int num_sms, cudaStream_t 
 // dlam from the records' D2 (dlam of a row is -D2), summed over what lam is broadcast over.
 struct DiffLamParams {
   const float* rec;
+  const float* sums;
   void* out;               // contiguous [B or 1][H or 1][NQ or 1]
   int B, H, NQ, NQpad;
   int eb, eh, en;          // extents of out

@@ -180,8 +180,9 @@ streamkl_status streamkl_diff_fwd(const streamkl_diff_problem* prob, const strea
 
 size_t streamkl_diff_bwd_workspace_size(const streamkl_diff_problem* prob) {
   if (check_diff(prob) != STREAMKL_OK) return 0;
-  return round256(static_cast<size_t>(prob->B) * prob->H * static_cast<size_t>(padded_rows(*prob)) *
-                  skl::kDiffRec * sizeof(float));
+  // row records, then a sum for every 64 rows
+  const size_t rows = static_cast<size_t>(prob->B) * prob->H * static_cast<size_t>(padded_rows(*prob));
+  return round256((rows * skl::kDiffRec + rows / skl::kDiffStep) * sizeof(float));
 }
 
 streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const streamkl_tensor* dO,
@@ -227,6 +228,7 @@ streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const strea
   pp.LSE1 = LSE1;
   pp.LSE2 = LSE2;
   pp.rec = rec;
+  pp.sums = rec + static_cast<size_t>(pr.B) * pr.H * padded_rows(pr) * skl::kDiffRec;
   pp.NQpad = padded_rows(pr);
   pp.dv = pr.dv;
   pp.f16 = f16;
@@ -236,6 +238,7 @@ streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const strea
   if (dlam) {
     skl::DiffLamParams lp;
     lp.rec = rec;
+    lp.sums = pp.sums;
     lp.out = dlam;
     lp.B = pr.B;
     lp.H = pr.H;

@@ -805,25 +805,41 @@ __global__ void __launch_bounds__(256) streamkl_diff_prep_kernel(const DiffPrepP
     __syncthreads();
     float* dst = p.rec + static_cast<long long>(u) * (CB * kDiffRec);
     for (int k = threadIdx.x; k < CB * kDiffRec; k += 256) dst[k] = out[k / CB][k % CB];
+    if (threadIdx.x < 32) {
+      float t = out[3][threadIdx.x] + out[3][threadIdx.x + 32];
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
+      if (threadIdx.x == 0) p.sums[u] = t;
+    }
     __syncthreads();
   }
 }
 
+template <class P>
+__device__ __forceinline__ void store_lam(const P& p, long long e, float v) {
+  if (p.f32) static_cast<float*>(p.out)[e] = v;
+  else if (p.f16) static_cast<__half*>(p.out)[e] = __float2half_rn(v);
+  else static_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16_rn(v);
+}
+
 // One block per element of dlam: -sum of D2 over the rows it is broadcast over,
 // each thread a strided share in order, then a tree: the same sum every time.
-__global__ void __launch_bounds__(512) streamkl_diff_lam_kernel(const DiffLamParams p) {
-  __shared__ float part[16];
-  const long long e = blockIdx.x;
-  const int n0 = static_cast<int>(e % p.en), h0 = static_cast<int>(e / p.en % p.eh),
-            b0 = static_cast<int>(e / p.en / p.eh);
-  const int nb = p.eb == 1 ? p.B : 1, nh = p.eh == 1 ? p.H : 1, nn = p.en == 1 ? p.NQ : 1;
-  const long long total = static_cast<long long>(nb) * nh * nn;
+// Where the rows of a sequence are all summed (en = 1), the 64-row sums of the
+// preparation are read in place of the rows.
+__global__ void __launch_bounds__(256) streamkl_diff_lam_kernel(const DiffLamParams p) {
+  __shared__ float part[8];
+  const int e = blockIdx.x;
+  const int n0 = e % p.en, h0 = e / p.en % p.eh, b0 = e / p.en / p.eh;
+  const int nb = p.eb == 1 ? p.B : 1, nh = p.eh == 1 ? p.H : 1;
+  const int steps = p.NQpad / CB;
   float s = 0.f;
-  for (long long k = threadIdx.x; k < total; k += blockDim.x) {
-    const int i = (p.en == 1 ? 0 : n0) + static_cast<int>(k % nn);
-    const long long q = k / nn;
-    const long long h = (p.eh == 1 ? 0 : h0) + q % nh, b = (p.eb == 1 ? 0 : b0) + q / nh;
-    s += p.rec[((b * p.H + h) * p.NQpad + (i / CB) * CB + 0) * kDiffRec + 3 * CB + i % CB];
+  for (int q = 0; q < nb * nh; ++q) {
+    const long long bh = static_cast<long long>(b0 + q / nh) * p.H + h0 + q % nh;
+    if (p.en == 1) {
+      for (int k = threadIdx.x; k < steps; k += blockDim.x) s += p.sums[bh * steps + k];
+    } else if (threadIdx.x == q % blockDim.x) {
+      s += p.rec[(bh * p.NQpad + (n0 / CB) * CB) * kDiffRec + 3 * CB + n0 % CB];
+    }
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
@@ -831,10 +847,8 @@ __global__ void __launch_bounds__(512) streamkl_diff_lam_kernel(const DiffLamPar
   __syncthreads();
   if (threadIdx.x == 0) {
     s = 0.f;
-    for (int k = 0; k < static_cast<int>(blockDim.x >> 5); ++k) s += part[k];
-    if (p.f32) static_cast<float*>(p.out)[e] = -s;
-    else if (p.f16) static_cast<__half*>(p.out)[e] = __float2half_rn(-s);
-    else static_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16_rn(-s);
+    for (int k = 0; k < 8; ++k) s += part[k];
+    store_lam(p, e, -s);
   }
 }
 
@@ -845,10 +859,7 @@ __global__ void __launch_bounds__(256) streamkl_diff_lam_rows_kernel(const DiffL
        e += static_cast<long long>(gridDim.x) * blockDim.x) {
     const int i = static_cast<int>(e % p.NQ);
     const long long bh = e / p.NQ;
-    const float s = -p.rec[(bh * p.NQpad + (i / CB) * CB) * kDiffRec + 3 * CB + i % CB];
-    if (p.f32) static_cast<float*>(p.out)[e] = s;
-    else if (p.f16) static_cast<__half*>(p.out)[e] = __float2half_rn(s);
-    else static_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16_rn(s);
+    store_lam(p, e, -p.rec[(bh * p.NQpad + (i / CB) * CB) * kDiffRec + 3 * CB + i % CB]);
   }
 }
 
@@ -880,7 +891,7 @@ cudaError_t launch_diff_lam(const DiffLamParams& p, cudaStream_t stream) {
     const long long blocks = (n + 255) / 256;
     streamkl_diff_lam_rows_kernel<<<static_cast<int>(blocks < 2048 ? blocks : 2048), 256, 0, stream>>>(p);
   } else {
-    streamkl_diff_lam_kernel<<<static_cast<unsigned>(n), 512, 0, stream>>>(p);
+    streamkl_diff_lam_kernel<<<static_cast<unsigned>(n), 256, 0, stream>>>(p);
   }
   return cudaGetLastError();
 }

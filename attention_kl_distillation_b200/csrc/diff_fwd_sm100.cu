@@ -53,8 +53,8 @@ struct FwdLay {
   static constexpr int ring_off = 2 * q_bytes;
   static constexpr int inv_off = ring_off + NS * slot_bytes;  // [2][R] fp32
   static constexpr int bar_off = inv_off + 2 * R * 4;
-  // full[NS] empty[NS] raw[NS] qfull qempty sfull[2] pfull[2] ofull oempty ifull drain
-  static constexpr int nbar = 3 * NS + 10;
+  // full[NS] empty[NS] raw[NS] qfull qempty sfull[2] pfull[2][2] ofull oempty ifull drain
+  static constexpr int nbar = 3 * NS + 12;
   static constexpr int misc_off = bar_off + nbar * 8;
   static constexpr int alloc = misc_off + 16 + 1024;
   static_assert(alloc <= 232448, "shared memory budget exceeded");
@@ -114,6 +114,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     streamkl_diff_fwd_kernel(const __grid_constant__ DiffFwdParams p) {
   using Lay = FwdLay<D>;
   constexpr int NS = Lay::NS;
+  // d = 64: the first 64 keys' value products start while the others' weights are
+  // formed (B1 H16 N8192 d64/128: 767 against 850 us).  At d = 128 the issuer has
+  // more products of the other map to give out and waiting twice costs more than
+  // it brings (B1 H16/4 N8192: 1012 against 938 us).
+  constexpr bool HALVES = D == 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -123,8 +128,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* qfull = raw + NS;
   uint64_t* qempty = qfull + 1;
   uint64_t* sfull = qempty + 1;  // [2] S_t of a tile is in TMEM (and PV_t of the one before is done)
-  uint64_t* pfull = sfull + 2;   // [2] P_t has replaced it
-  uint64_t* ofull = pfull + 2;
+  uint64_t* pfull = sfull + 2;   // [map][half] 64 keys of P_t are in its place
+  uint64_t* ofull = pfull + 4;
   uint64_t* oempty = ofull + 1;
   uint64_t* ifull = oempty + 1;  // both maps' 1/l are in shared memory
   uint64_t* drain = ifull + 1;
@@ -147,7 +152,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(qempty, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
-      mbar_init(&pfull[t], 4);
+      mbar_init(&pfull[2 * t], 4);
+      mbar_init(&pfull[2 * t + 1], 4);
     }
     mbar_init(ofull, 1);
     mbar_init(oempty, 8);
@@ -245,12 +251,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             w16[j >> 1] = pack2<F16>(e.x, e.y);
           }
           tmem_st_32x32b_x16(scol + q * 16, w16);
+          if (q == 3 || (HALVES && q == 1)) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[2 * t + (HALVES ? q >> 1 : 0)]);
+          }
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[t]);
       }
       if (!ok) break;
       // Epilogue: the maps exchange 1/l_t, then each warpgroup forms half the columns.
@@ -421,12 +429,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           umma_commit(&sfull[t]);
         };
-        auto issue_pv = [&](int t, uint8_t* tile, bool first) {
+        // PV_t, each half of the keys as soon as its weights are there
+        auto issue_pv = [&](int t, uint8_t* tile, bool first) -> bool {
           const uint64_t vd = sdesc_sw128(smem_u32(tile), BK * 128, 1024);
-  #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            if (kk == 0 || (HALVES && kk == 4)) {
+              if (!mbar_wait(&pfull[2 * t + kk / 4], pph, ctl)) return false;
+              tc_fence_after();
+            }
             umma_bf16_ts(tmem + kColO + t * 128, tmem + t * BK + kk * 8, sdesc_advance(vd, kk * 2048),
                          idO, !first || kk > 0);
+          }
+          return true;
         };
         while (ok && sched.next(u)) {
           const FwdUnit w = decode(p, u);
@@ -460,9 +475,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               if (!(ok = mbar_wait(oempty, oph ^ 1, ctl))) break;
               oph ^= 1;
             }
-            if (!(ok = mbar_wait(&pfull[0], pph, ctl))) break;
-            tc_fence_after();
-            issue_pv(0, slot_s(sv), kt == 0);
+            if (!(ok = issue_pv(0, slot_s(sv), kt == 0))) break;
             if (more) {
               if (!(ok = mbar_wait(&full[s], ph, ctl))) break;
               tc_fence_after();
@@ -472,10 +485,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 step();
               }
             }
-            if (!(ok = mbar_wait(&pfull[1], pph, ctl))) break;
+            if (!(ok = issue_pv(1, slot_s(sv), kt == 0))) break;
             pph ^= 1;
-            tc_fence_after();
-            issue_pv(1, slot_s(sv), kt == 0);
             umma_commit(&empty[sv]);
             if (more) {
               if constexpr (D == 64) {
