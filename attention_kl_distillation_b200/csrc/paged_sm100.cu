@@ -152,7 +152,13 @@ __device__ void tile_line(const PagedParams& p, int items, int* cum, int* scratc
 // A position on the line of tiles.
 struct Cursor {
   int b, item, tile, ntiles, len;  // item within the sequence; ntiles of one item
-  __device__ __forceinline__ void seek(const PagedParams& p, const int* cum, int items, int t) {
+  int hk, first;                   // the item's key head, and first query head of its block
+  __device__ __forceinline__ void head(int blocks) {
+    hk = item / blocks;
+    first = (item - hk * blocks) * HB;
+  }
+  __device__ __forceinline__ void seek(const PagedParams& p, const int* cum, int items, int blocks,
+                                       int t) {
     int lo = 0, hi = p.B - 1;  // the sequence with cum[b] <= t < cum[b + 1]
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -164,12 +170,17 @@ struct Cursor {
     item = (t - cum[b]) / ntiles;
     tile = (t - cum[b]) % ntiles;
     len = paged_len(p, b);
+    head(blocks);
   }
-  __device__ __forceinline__ void advance(const PagedParams& p, const int* cum, int items) {
+  __device__ __forceinline__ void advance(const PagedParams& p, const int* cum, int items, int blocks) {
     if (++tile < ntiles) return;
     tile = 0;
-    if (++item < items) return;
+    if (++item < items) {
+      head(blocks);
+      return;
+    }
     item = 0;
+    head(blocks);
     do ++b;
     while (b < p.B && cum[b + 1] == cum[b]);
     if (b < p.B) {
@@ -293,8 +304,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
     streamkl_paged_kernel(const __grid_constant__ PagedParams p) {
   using Lay = PagedLay<D, DV, MAPS>;
   constexpr int NST = Lay::NST, WPT = Lay::WPT, MT = Lay::MT;
-  constexpr int KP = D / 8, VP = DV / 8;  // 16-byte pieces of a row
-  extern __shared__ __align__(128) uint8_t smem_paged[];
+  constexpr int VP = DV / 8;       // 16-byte pieces of a row
+  constexpr int CHUNK = KT * 128;  // bytes of 64 features of a tile
+  extern __shared__ __align__(1024) uint8_t smem_paged[];
   __shared__ int scratch[NW];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team = warp / WPT, member = warp % WPT;
@@ -341,22 +353,35 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const int slot = page_row(token(cur));
     const uint32_t seen = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
     if (member == 0 && lane == 0) masks[s] = seen;
-    const int hk = cur.item / blocks;
-    auto copy = [&](const PagedCache& cache, uint32_t dst, int pieces) {
-      const uint16_t* base = static_cast<const uint16_t*>(cache.ptr) + hk * cache.head;
-      const long long row = page * cache.page + slot * cache.row;  // of this lane's row
-#pragma unroll
-      for (int i = member; i < KT * pieces / 32; i += WPT) {
-        const int idx = i * 32 + lane, r = idx / pieces, q = idx % pieces;
-        const long long off = __shfl_sync(0xffffffffu, row, r);
-        const bool ok = (seen >> r) & 1u;
-        cp_async16(dst + r * pieces * 16 + ((q ^ (r & 7)) * 16), base + (ok ? off + q * 8 : 0), ok ? 16 : 0);
-      }
-    };
+    // Eight lanes copy 128 bytes of a row at a time, four rows in turn.  The
+    // layout: chunks of 64 features, 16 rows of 128 bytes each, 16-byte pieces
+    // exchanged by the row's low three bits (ldmatrix then meets no bank twice).
+    const uint16_t* k1 = static_cast<const uint16_t*>(p.K1.ptr) + cur.hk * p.K1.head + (lane & 7) * 8;
+    const uint16_t* k2 = static_cast<const uint16_t*>(p.K2.ptr) + cur.hk * p.K2.head + (lane & 7) * 8;
+    const uint16_t* v = static_cast<const uint16_t*>(p.V.ptr) + cur.hk * p.V.head + (lane & 7) * 8;
     const uint32_t a = ring_a + s * Lay::stage;
-    copy(p.K1, a, KP);
-    if (MAPS == 2) copy(p.K2, a + Lay::k_bytes, KP);
-    copy(p.V, a + MAPS * Lay::k_bytes, VP);
+#pragma unroll
+    for (int i = 0; i < KT / 4; ++i) {
+      if (WPT == 2 && (i & 1) != member) continue;  // the team's warps take turns
+      const int r = i * 4 + (lane >> 3);
+      const int pg = __shfl_sync(0xffffffffu, page, r), sl = __shfl_sync(0xffffffffu, slot, r);
+      const bool ok = pg >= 0;
+      const long long pgl = ok ? pg : 0, sll = ok ? sl : 0;  // what is not read still has an address
+      const int bytes = ok ? 16 : 0;
+      const uint32_t dst = a + r * 128 + (((lane & 7) ^ (r & 7)) * 16);
+      const uint16_t* src = k1 + pgl * p.K1.page + sll * p.K1.row;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) cp_async16(dst + c * CHUNK, src + c * 64, bytes);
+      if (MAPS == 2) {
+        src = k2 + pgl * p.K2.page + sll * p.K2.row;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) cp_async16(dst + Lay::k_bytes + c * CHUNK, src + c * 64, bytes);
+      }
+      src = v + pgl * p.V.page + sll * p.V.row;
+#pragma unroll
+      for (int c = 0; c < DV / 64; ++c)
+        cp_async16(dst + MAPS * Lay::k_bytes + c * CHUNK, src + c * 64, bytes);
+    }
   };
   auto team_sync = [&]() {
     if (WPT == 1) __syncwarp();
@@ -364,7 +389,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   };
 
   Cursor ld, cur;
-  ld.seek(p, cum, items, t0);
+  ld.seek(p, cum, items, blocks, t0);
   cur = ld;
   int tl = t0;  // next tile to be issued
   int page = page_of(ld);
@@ -373,7 +398,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
       issue(ld, page, s);
       ++tl;
       if (tl < t1) {
-        ld.advance(p, cum, items);
+        ld.advance(p, cum, items, blocks);
         page = page_of(ld);
       }
     }
@@ -385,7 +410,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   State<MAPS, MT> st;
   uint32_t qf[MAPS][D / 16][2];
   auto load_q = [&]() {
-    const int hk = cur.item / blocks, k = (cur.item % blocks) * HB + (lane >> 2);
+    const int hk = cur.hk, k = cur.first + (lane >> 2);
 #pragma unroll
     for (int t = 0; t < MAPS; ++t) {
       const uint16_t* q = t ? static_cast<const uint16_t*>(p.Q2) + cur.b * p.q2_b + (hk * g + k) * p.q2_h
@@ -401,6 +426,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
   st.clear();
   load_q();
 
+  // This lane's row and piece of an ldmatrix: keys as they lie (rows lane % 16,
+  // features 8 (lane / 16) on), values transposed (rows lane % 8 + 8 (lane / 16),
+  // features 8 (lane / 8 % 2) on).  Further features are an exclusive or away.
+  const uint32_t k_lane = (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) * 16);
+  const uint32_t v_lane = ((lane & 7) + ((lane >> 4) << 3)) * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
   int s = 0;
   for (int t = t0; t < t1; ++t) {
     cp_async_wait<NST - 2>();
@@ -408,58 +438,79 @@ __global__ void __launch_bounds__(NW * 32, 1)
     issue_next(s == 0 ? NST - 1 : s - 1);  // the stage read in the last round
     const uint32_t a = ring_a + s * Lay::stage;
     const uint32_t seen = masks[s];
-    uint32_t pf[MAPS][2];
+    if (seen) {
+      // S^T of both maps: keys lane/4 (+8), heads 2c, 2c+1
+      float x[MAPS][4];
 #pragma unroll
-    for (int m = 0; m < MAPS; ++m) {
-      // S^T: keys lane/4 (+8), heads 2c, 2c+1
-      float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
-      const int r = lane & 15;
+      for (int m = 0; m < MAPS; ++m) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t af[4];
-        ldsm4(a + m * Lay::k_bytes + r * (D * 2) + (((kk * 2 + (lane >> 4)) ^ (r & 7)) * 16), af);
-        mma16816<F16>((kk & 1) ? sd : sc, af, qf[m][kk][0], qf[m][kk][1]);
-      }
-      const float cm = m ? p.c2 : p.c1;
-      float x[4];
+        for (int e = 0; e < 4; ++e) x[m][e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        x[e] = ((seen >> ((lane >> 2) + (e >> 1) * 8)) & 1u) ? (sc[e] + sd[e]) * cm : -INFINITY;
-      float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
-      if (__any_sync(0xffffffffu, mx[0] > st.m[m][0] + kSlack || mx[1] > st.m[m][1] + kSlack)) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
-          const bool grow = mx[e] > st.m[m][e] + kSlack;
-          const float f = grow ? ex2(st.m[m][e] - mx[e]) : 1.f;
-          if (grow) st.m[m][e] = mx[e];
-          st.l[m][e] *= f;
-#pragma unroll
-          for (int q = 0; q < MT; ++q) {
-            st.o[m][q][e] *= f;
-            st.o[m][q][e + 2] *= f;
-          }
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t af[4];
+          ldsm4(((a + k_lane) ^ ((kk & 3) * 32)) + m * Lay::k_bytes + (kk >> 2) * CHUNK, af);
+          mma16816<F16>(x[m], af, qf[m][kk][0], qf[m][kk][1]);
         }
       }
+      if (seen != 0xffffu) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float ref = st.m[m][e & 1] == -INFINITY ? 0.f : st.m[m][e & 1];
-        x[e] = ex2(x[e] - ref);
-        st.l[m][e & 1] += x[e];
+        for (int e = 0; e < 4; ++e) {
+          const bool ok = (seen >> ((lane >> 2) + (e >> 1) * 8)) & 1u;
+#pragma unroll
+          for (int m = 0; m < MAPS; ++m) x[m][e] = ok ? x[m][e] : -INFINITY;
+        }
       }
-      // P^T as the B operand: heads on rows after the transposition
-      pf[m][0] = transpose8x8(pack2<F16>(x[0], x[1]));
-      pf[m][1] = transpose8x8(pack2<F16>(x[2], x[3]));
-    }
+      bool grow = false;
+      float mx[MAPS][2];
 #pragma unroll
-    for (int q = 0; q < MT; ++q) {
-      uint32_t vf[4];
-      const int r = (lane & 7) + ((lane >> 4) << 3);
-      const int piece = member * (Lay::DVW / 8) + q * 2 + ((lane >> 3) & 1);
-      ldsm4_t(a + MAPS * Lay::k_bytes + r * (DV * 2) + ((piece ^ (r & 7)) * 16), vf);
+      for (int m = 0; m < MAPS; ++m)
 #pragma unroll
-      for (int m = 0; m < MAPS; ++m) mma16816<F16>(st.o[m][q], vf, pf[m][0], pf[m][1]);
+        for (int e = 0; e < 2; ++e) {
+          mx[m][e] = fmaxf(x[m][e], x[m][e + 2]) * (m ? p.c2 : p.c1);
+          grow = grow || mx[m][e] > st.m[m][e] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int m = 0; m < MAPS; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1)
+              mx[m][e] = fmaxf(mx[m][e], __shfl_xor_sync(0xffffffffu, mx[m][e], d));
+            const bool up = mx[m][e] > st.m[m][e] + kSlack;
+            const float f = up ? ex2(st.m[m][e] - mx[m][e]) : 1.f;
+            if (up) st.m[m][e] = mx[m][e];
+            st.l[m][e] *= f;
+#pragma unroll
+            for (int q = 0; q < MT; ++q) {
+              st.o[m][q][e] *= f;
+              st.o[m][q][e + 2] *= f;
+            }
+          }
+      }
+      uint32_t pf[MAPS][2];
+#pragma unroll
+      for (int m = 0; m < MAPS; ++m) {
+        const float cm = m ? p.c2 : p.c1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float ref = st.m[m][e & 1] == -INFINITY ? 0.f : st.m[m][e & 1];
+          x[m][e] = ex2(fmaf(x[m][e], cm, -ref));
+          st.l[m][e & 1] += x[m][e];
+        }
+        // P^T as the B operand: heads on rows after the transposition
+        pf[m][0] = transpose8x8(pack2<F16>(x[m][0], x[m][1]));
+        pf[m][1] = transpose8x8(pack2<F16>(x[m][2], x[m][3]));
+      }
+#pragma unroll
+      for (int q = 0; q < MT; ++q) {
+        uint32_t vf[4];
+        ldsm4_t(((a + v_lane) ^ ((q & 3) * 32)) + MAPS * Lay::k_bytes +
+                    (member * (Lay::DVW / 64) + (q >> 2)) * CHUNK,
+                vf);
+#pragma unroll
+        for (int m = 0; m < MAPS; ++m) mma16816<F16>(st.o[m][q], vf, pf[m][0], pf[m][1]);
+      }
     }
     if (++s == NST) s = 0;
 
@@ -472,23 +523,24 @@ __global__ void __launch_bounds__(NW * 32, 1)
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) st.l[m][e] += __shfl_xor_sync(0xffffffffu, st.l[m][e], d);
+      const Cursor at = cur;
+      const bool begun_here = item_start >= t0;
+      if (t + 1 < t1) {  // the next item's queries are on their way while this one is joined
+        cur.advance(p, cum, items, blocks);
+        item_start = t + 1;
+        load_q();
+      }
       join_warps<Lay>(st, buf, warp, lane);
       if (team == 0) {
-        const int hk = cur.item / blocks, first = (cur.item % blocks) * HB;
-        if (item_start >= t0 && item_ends) {
-          st.template finish<F16>(p, cur.b, hk * g + first, min(HB, g - first), member * Lay::DVW, lane);
+        if (begun_here && item_ends) {
+          st.template finish<F16>(p, at.b, at.hk * g + at.first, min(HB, g - at.first), member * Lay::DVW, lane);
         } else {
           // begun before this stretch: slot 2c; going on behind it: slot 2c + 1
-          const long long slot = 2ll * c + (item_start >= t0 ? 1 : 0);
+          const long long slot = 2ll * c + (begun_here ? 1 : 0);
           st.put(p.part + slot * Lay::slot_floats + member * Lay::image, lane);
         }
       }
-      if (t + 1 < t1) {
-        cur.advance(p, cum, items);
-        item_start = t + 1;
-        st.clear();
-        load_q();
-      }
+      st.clear();
     } else {
       ++cur.tile;
     }
@@ -521,7 +573,7 @@ __global__ void __launch_bounds__(NW * 32)
   const int cut = static_cast<int>(stretch_start(total, c, n));
   const int before = static_cast<int>(stretch_start(total, c - 1, n));
   Cursor cur;
-  cur.seek(p, cum, items, cut);
+  cur.seek(p, cum, items, blocks, cut);
   const int start = cut - cur.tile, end = start + cur.ntiles;
   if (start == cut || start < before) return;  // no item is cut here, or an earlier cut has it
   State<MAPS, Lay::MT> st;
@@ -533,7 +585,7 @@ __global__ void __launch_bounds__(NW * 32)
   }
   join_warps<Lay>(st, buf, warp, lane);
   if (team != 0) return;
-  const int hk = cur.item / blocks, first = (cur.item % blocks) * HB;
+  const int hk = cur.hk, first = cur.first;
   st.template finish<F16>(p, cur.b, hk * g + first, min(HB, g - first), member * Lay::DVW, lane);
 }
 
