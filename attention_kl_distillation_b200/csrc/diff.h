@@ -140,9 +140,11 @@ struct PagedParams {
   int B, H, HK, pages, page_size, max_pages;
   int page_shift;            // log2(page_size), or -1 when it is no power of two
   float c1, c2;
-  float* part;               // workspace
+  int4* cuts;                // workspace: a record per CTA, then the partial states
+  float* part;
   int* status;
 };
+size_t paged_cuts_bytes(int num_sms);
 size_t paged_workspace_bytes(int dv, int maps, int num_sms);
 cudaError_t launch_paged(const PagedParams& p, int d, int dv, bool f16, int num_sms,
                          cudaStream_t stream);

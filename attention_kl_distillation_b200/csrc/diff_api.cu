@@ -113,9 +113,10 @@ streamkl_status check_paged(const streamkl_paged_problem* pr) {
   if (pr->B > 4096) return STREAMKL_EINVAL;
   const int64_t most = static_cast<int64_t>(pr->max_pages) * pr->page_size;
   if (most > (1 << 30)) return STREAMKL_EINVAL;
-  // tiles of 64 keys or more, per key head and block of 8 query heads, in int
+  // Tiles are counted in int.  One holds 64 tokens of a work item (a key head, 8 of its
+  // query heads) or more, or a share of them of several items.
   const int64_t items = static_cast<int64_t>(pr->HK) * ((pr->H / pr->HK + 7) / 8);
-  if (items > (1 << 20) || pr->B * items * ((most + 63) / 64) > INT32_MAX) return STREAMKL_EINVAL;
+  if (items > (1 << 20) || pr->B * items * (most / 64 + 1) > INT32_MAX) return STREAMKL_EINVAL;
   if (pr->dtype != STREAMKL_BF16 && pr->dtype != STREAMKL_FP16) return STREAMKL_EUNSUPPORTED;
   if (!widths_ok(pr->d, pr->dv)) return STREAMKL_EUNSUPPORTED;
   return STREAMKL_OK;
@@ -375,7 +376,8 @@ streamkl_status streamkl_paged_attn(const streamkl_paged_problem* prob, const st
     if (pr.page_size == 1 << k) p.page_shift = k;
   p.c1 = scale_of(pr.s1, pr.d) * kLog2e;
   p.c2 = scale_of(pr.s2, pr.d) * kLog2e;
-  p.part = static_cast<float*>(workspace);
+  p.cuts = static_cast<int4*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + skl::paged_cuts_bytes(sms));
   if (skl::launch_paged(p, pr.d, pr.dv, pr.dtype == STREAMKL_FP16, sms,
                         reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return STREAMKL_ECUDA;

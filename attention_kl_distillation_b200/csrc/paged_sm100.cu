@@ -13,8 +13,15 @@
 // padding of 8 heads to 128 rows) and each warp streams its own keys through
 // cp.async without a barrier among warps.
 //
-// Work split: a tile is 16 keys per team of warps, 128 (dv = 256: 64) per CTA.
-// The tiles of all sequences and key heads form one line, cut into equal
+// Work split: a team (a warp; dv = 256: two, each with 128 value columns) takes
+// 16 keys of one work item at a time, an item being a key head and up to 8 of
+// the query heads that share it.  The teams of a CTA take neighbouring items of
+// a sequence (HW of them, as many as divide the items) at the same tokens:
+// together they read whole rows of the cache, [token][head][feature], where one
+// head's 128 or 256 bytes at a time would use a fraction of each DRAM page
+// (B32 H16 d64/128, 2048 tokens each: HW_FIGURES).  Where HW is less than
+// the teams, they also split the tokens, and are joined at an item's end.
+// The tiles of all sequences and groups of items form one line, cut into equal
 // stretches, one per CTA: lengths may differ by any factor and every CTA still
 // reads the same number of rows.  The cut is computed on the device from lens,
 // so a captured graph stays right when lengths change.  A stretch may hold
@@ -29,6 +36,7 @@ constexpr int KT = 16;       // keys per team and tile
 constexpr int NW = 8;        // warps per CTA
 constexpr int HB = 8;        // query heads per work item (mma N)
 constexpr int kMaxBatch = 4096;
+constexpr int kJoinThreads = 512;
 constexpr int kBehind = -2147483647 - 1;
 constexpr float kSlack = 8.f;  // a reference grows only by more than this (log2)
 
@@ -38,7 +46,6 @@ struct PagedLay {
   static constexpr int TEAMS = NW / WPT;
   static constexpr int DVW = DV / WPT;
   static constexpr int MT = DVW / 16;           // value m-tiles per warp
-  static constexpr int TILE = KT * TEAMS;       // keys per CTA tile
   static constexpr int k_bytes = KT * D * 2;
   static constexpr int v_bytes = KT * DV * 2;
   static constexpr int stage = MAPS * k_bytes + v_bytes;
@@ -46,16 +53,17 @@ struct PagedLay {
   static constexpr int NST = fit > 6 ? 6 : fit;
   static constexpr int NREG = MAPS * MT * 4;    // output registers per lane
   static constexpr int ring = NST * stage * TEAMS;
-  static constexpr int buf = 2 * 32 * (NREG + 4 * MAPS) * 4;  // two warps' states at a time
+  static constexpr int frag = 32 * (NREG + 4 * MAPS);      // floats of one warp's state
+  static constexpr int buf = 2 * frag * 4;                 // two warps' states at a time
   static constexpr int buf_off = ring;
   static constexpr int mask_off = buf_off + buf;
   static constexpr int cum_off = mask_off + NST * TEAMS * 4;
   static constexpr int alloc(int B) { return cum_off + (B + 1) * 4; }
   static_assert(NST >= 2, "ring too shallow");
   static_assert(cum_off + (kMaxBatch + 1) * 4 <= 232448, "shared memory budget exceeded");
-  // Workspace of one stretch end: outputs and (m, l) per map and head, in the
-  // fragment order of the warps of a team.
-  static constexpr int image = 32 * (NREG + 4 * MAPS);  // floats of one warp's state
+  // Workspace of one stretch end and team: outputs and (m, l) per map and head, in
+  // the fragment order of its warps.
+  static constexpr int image = 32 * NREG + 2 * MAPS * HB;  // floats of one warp's part, 8 heads
   static constexpr int slot_floats = WPT * image;
 };
 
@@ -102,6 +110,23 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// How a problem's work items are dealt to `grid` CTAs: `groups` groups of `hw`
+// items a sequence, `tile` tokens per tile of the line.  Every cut through a
+// group costs a state of each of its items, so a group is no wider than leaves
+// about half as many groups as CTAs.
+struct Deal {
+  int g, blocks, hw, groups, tile;
+  __device__ __forceinline__ Deal(const PagedParams& p, int teams, int grid) {
+    g = p.H / p.HK;
+    blocks = (g + HB - 1) / HB;
+    const int items = p.HK * blocks;
+    hw = teams;
+    while (hw > 1 && (items % hw != 0 || 2 * p.B * (items / hw) < grid)) hw >>= 1;
+    groups = items / hw;
+    tile = KT * teams / hw;
+  }
+};
+
 // Tokens of sequence b that are attended to: lens[b] within the table.
 __device__ __forceinline__ int paged_len(const PagedParams& p, int b) {
   const long long most = static_cast<long long>(p.max_pages) * p.page_size;
@@ -117,25 +142,23 @@ __device__ __forceinline__ long long stretch_start(long long total, int c, int n
   return total * c / n;
 }
 
-// cum[b] = tiles of the work items of sequences before b; cum[B] the total.
-// Items of a sequence: (key head, block of HB query heads), each of its tiles.
-template <int TILE>
-__device__ void tile_line(const PagedParams& p, int items, int* cum, int* scratch) {
+// cum[b] = tiles of the sequences before b; cum[B] the total.
+__device__ void tile_line(const PagedParams& p, const Deal& d, int* cum, int* scratch) {
   const int tid = threadIdx.x, nt = blockDim.x;
   const int per = (p.B + nt - 1) / nt;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   int s = 0;
   for (int b = b0; b < b1; ++b) {
-    const int t = (paged_len(p, b) + TILE - 1) / TILE * items;
+    const int t = (paged_len(p, b) + d.tile - 1) / d.tile * d.groups;
     cum[b + 1] = t;
     s += t;
   }
   const int lane = tid & 31, warp = tid >> 5;
   int x = s;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
+  for (int k = 1; k < 32; k <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, k);
+    if (lane >= k) x += y;
   }
   if (lane == 31) scratch[warp] = x;
   __syncthreads();
@@ -149,16 +172,17 @@ __device__ void tile_line(const PagedParams& p, int items, int* cum, int* scratc
   __syncthreads();
 }
 
-// A position on the line of tiles.
+// A position on the line of tiles, for one team: its item within the group is
+// team % hw, its tokens of a tile are those from 16 (team / hw) on.
 struct Cursor {
-  int b, item, tile, ntiles, len;  // item within the sequence; ntiles of one item
-  int hk, first;                   // the item's key head, and first query head of its block
-  __device__ __forceinline__ void head(int blocks) {
-    hk = item / blocks;
-    first = (item - hk * blocks) * HB;
+  int b, group, tile, ntiles, len;  // ntiles of one group
+  int hk, first;                    // the item's key head, and first query head of its block
+  __device__ __forceinline__ void head(const Deal& d, int team) {
+    const int item = group * d.hw + (team & (d.hw - 1));
+    hk = item / d.blocks;
+    first = (item - hk * d.blocks) * HB;
   }
-  __device__ __forceinline__ void seek(const PagedParams& p, const int* cum, int items, int blocks,
-                                       int t) {
+  __device__ __forceinline__ void seek(const PagedParams& p, const int* cum, const Deal& d, int team, int t) {
     int lo = 0, hi = p.B - 1;  // the sequence with cum[b] <= t < cum[b + 1]
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -166,25 +190,25 @@ struct Cursor {
       else hi = mid - 1;
     }
     b = lo;
-    ntiles = (cum[b + 1] - cum[b]) / items;
-    item = (t - cum[b]) / ntiles;
+    ntiles = (cum[b + 1] - cum[b]) / d.groups;
+    group = (t - cum[b]) / ntiles;
     tile = (t - cum[b]) % ntiles;
     len = paged_len(p, b);
-    head(blocks);
+    head(d, team);
   }
-  __device__ __forceinline__ void advance(const PagedParams& p, const int* cum, int items, int blocks) {
+  __device__ __forceinline__ void advance(const PagedParams& p, const int* cum, const Deal& d, int team) {
     if (++tile < ntiles) return;
     tile = 0;
-    if (++item < items) {
-      head(blocks);
+    if (++group < d.groups) {
+      head(d, team);
       return;
     }
-    item = 0;
-    head(blocks);
+    group = 0;
+    head(d, team);
     do ++b;
     while (b < p.B && cum[b + 1] == cum[b]);
     if (b < p.B) {
-      ntiles = (cum[b + 1] - cum[b]) / items;
+      ntiles = (cum[b + 1] - cum[b]) / d.groups;
       len = paged_len(p, b);
     }
   }
@@ -210,7 +234,8 @@ struct State {
       }
     }
   }
-  // fragment-order image, one float per lane at a stride of 32
+  // Image in fragment order, for another warp of this CTA: one float per lane at
+  // a stride of 32.
   __device__ __forceinline__ void put(float* dst, int lane) const {
     int k = 0;
 #pragma unroll
@@ -227,7 +252,7 @@ struct State {
         dst[32 * k++ + lane] = l[t][e];
       }
   }
-  // joins another state's image: both sides rescaled to the larger reference
+  // joins another warp's image: both sides rescaled to the larger reference
   __device__ __forceinline__ void join(const float* src, int lane) {
     const float* ml = src + 32 * (MAPS * MT * 4);
 #pragma unroll
@@ -248,6 +273,29 @@ struct State {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           o[t][q][e] = fmaf(o[t][q][e], fa[e & 1], src[32 * ((t * MT + q) * 4 + e) + lane] * fb[e & 1]);
+    }
+  }
+  // Part of the first `heads` heads for the second kernel: per map, value row and
+  // head as they lie in the outputs' order [8 rows][head][8], then (m, l) per map
+  // and head.
+  __device__ __forceinline__ void put_part(float* dst, int heads, int lane) const {
+    float* ml = dst + MAPS * MT * 16 * heads;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int h = (lane & 3) * 2 + e;
+      if (h >= heads) continue;
+#pragma unroll
+      for (int t = 0; t < MAPS; ++t) {
+#pragma unroll
+        for (int q = 0; q < MT; ++q) {
+          dst[((t * MT + q) * 2 * heads + h) * 8 + (lane >> 2)] = o[t][q][e];
+          dst[(((t * MT + q) * 2 + 1) * heads + h) * 8 + (lane >> 2)] = o[t][q][e + 2];
+        }
+        if (lane < 4) {
+          ml[(t * heads + h) * 2] = m[t][e];
+          ml[(t * heads + h) * 2 + 1] = l[t][e];
+        }
+      }
     }
   }
   // O_1/l_1 - lam O_2/l_2 of the heads first..first+HB-1 below `heads`
@@ -283,20 +331,23 @@ struct State {
   }
 };
 
-// Joins the states of all warps into those of the first team, in a fixed order,
-// through a buffer of two warps' states.
+// Joins the states of teams that differ by a multiple of `hw` into those of the
+// first hw teams, in a fixed order, through a buffer of two warps' states.
 template <class Lay, class S>
-__device__ __forceinline__ void join_warps(S& st, float* buf, int warp, int lane) {
+__device__ __forceinline__ void join_teams(S& st, float* buf, int warp, int lane, int hw) {
   auto hand = [&](int from, int to, int count) {  // warps [from, from + count) to [to, ..)
     __syncthreads();
-    if (warp >= from && warp < from + count) st.put(buf + (warp - from) * Lay::image, lane);
+    if (warp >= from && warp < from + count) st.put(buf + (warp - from) * Lay::frag, lane);
     __syncthreads();
-    if (warp >= to && warp < to + count) st.join(buf + (warp - to) * Lay::image, lane);
+    if (warp >= to && warp < to + count) st.join(buf + (warp - to) * Lay::frag, lane);
   };
-  hand(4, 0, 2);
-  hand(6, 2, 2);
-  hand(2, 0, 2);
-  if (Lay::WPT == 1) hand(1, 0, 1);
+  const int keep = hw * Lay::WPT;  // warps that end up with an item's state
+  if (keep <= 4) {
+    hand(4, 0, 2);
+    hand(6, 2, 2);
+  }
+  if (keep <= 2) hand(2, 0, 2);
+  if (keep <= 1) hand(1, 0, 1);
 }
 
 template <int D, int DV, int MAPS, bool F16>
@@ -316,8 +367,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
   int* cum = reinterpret_cast<int*>(smem_paged + Lay::cum_off);
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int g = p.H / p.HK, blocks = (g + HB - 1) / HB, items = p.HK * blocks;
-  tile_line<Lay::TILE>(p, items, cum, scratch);
+  const Deal deal(p, Lay::TEAMS, gridDim.x);
+  tile_line(p, deal, cum, scratch);
   const long long total = cum[p.B];
   const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
   const int c = blockIdx.x;
@@ -329,15 +380,19 @@ __global__ void __launch_bounds__(NW * 32, 1)
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O) + b * p.o_b + (k / VP) * p.o_h +
                                 (k % VP) * 8) = make_uint4(0u, 0u, 0u, 0u);
   }
-  if (c >= n) return;
+  if (c >= n) {
+    if (threadIdx.x == 0) p.cuts[c] = make_int4(0, 0, 0, 0);
+    return;
+  }
   const int t0 = static_cast<int>(stretch_start(total, c, n));
   const int t1 = static_cast<int>(stretch_start(total, c + 1, n));
 
   const uint32_t ring_a = smem_u32(ring);
+  const int g = deal.g, kw = team / deal.hw, mine = team & (deal.hw - 1);  // item of the group
   // Page and row of token tok; page sizes are mostly powers of two.
   auto page_index = [&](int tok) { return p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size; };
   auto page_row = [&](int tok) { return p.page_shift >= 0 ? tok & (p.page_size - 1) : tok % p.page_size; };
-  auto token = [&](const Cursor& cur) { return cur.tile * Lay::TILE + team * KT + (lane & 15); };
+  auto token = [&](const Cursor& cur) { return cur.tile * deal.tile + kw * KT + (lane & 15); };
   // Lane r (and r + 16) reads the table entry of row r a tile ahead of its use;
   // what it holds is looked at only then.  kBehind: no such token.
   auto page_of = [&](const Cursor& cur) -> int {
@@ -389,8 +444,17 @@ __global__ void __launch_bounds__(NW * 32, 1)
   };
 
   Cursor ld, cur;
-  ld.seek(p, cum, items, blocks, t0);
+  ld.seek(p, cum, deal, team, t0);
   cur = ld;
+  // For the second kernel: the group of items that the cut in front of this
+  // stretch goes through, if it is the first cut through it, and its parts.
+  if (c > 0 && threadIdx.x == 0) {
+    const int start = t0 - cur.tile, end = start + cur.ntiles;
+    int parts = 0;
+    if (cur.tile > 0 && start >= static_cast<int>(stretch_start(total, c - 1, n)))
+      for (parts = 2; c - 1 + parts < n && stretch_start(total, c - 1 + parts, n) < end;) ++parts;
+    p.cuts[c] = make_int4(cur.b, cur.group, parts, 0);
+  }
   int tl = t0;  // next tile to be issued
   int page = page_of(ld);
   auto issue_next = [&](int s) {
@@ -398,7 +462,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
       issue(ld, page, s);
       ++tl;
       if (tl < t1) {
-        ld.advance(p, cum, items, blocks);
+        ld.advance(p, cum, deal, team);
         page = page_of(ld);
       }
     }
@@ -516,7 +580,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
 
     const bool item_ends = cur.tile + 1 == cur.ntiles;
     if (item_ends || t + 1 == t1) {
-      // The warps' states of this item, joined in a fixed order.
+      // This stretch's part of the group's items.
 #pragma unroll
       for (int m = 0; m < MAPS; ++m)
 #pragma unroll
@@ -525,19 +589,20 @@ __global__ void __launch_bounds__(NW * 32, 1)
           for (int d = 4; d < 32; d <<= 1) st.l[m][e] += __shfl_xor_sync(0xffffffffu, st.l[m][e], d);
       const Cursor at = cur;
       const bool begun_here = item_start >= t0;
+      const int heads = min(HB, g - at.first);
       if (t + 1 < t1) {  // the next item's queries are on their way while this one is joined
-        cur.advance(p, cum, items, blocks);
+        cur.advance(p, cum, deal, team);
         item_start = t + 1;
         load_q();
       }
-      join_warps<Lay>(st, buf, warp, lane);
-      if (team == 0) {
+      if (deal.hw < Lay::TEAMS) join_teams<Lay>(st, buf, warp, lane, deal.hw);
+      if (kw == 0) {
         if (begun_here && item_ends) {
-          st.template finish<F16>(p, at.b, at.hk * g + at.first, min(HB, g - at.first), member * Lay::DVW, lane);
+          st.template finish<F16>(p, at.b, at.hk * g + at.first, heads, member * Lay::DVW, lane);
         } else {
           // begun before this stretch: slot 2c; going on behind it: slot 2c + 1
-          const long long slot = 2ll * c + (begun_here ? 1 : 0);
-          st.put(p.part + slot * Lay::slot_floats + member * Lay::image, lane);
+          const long long slot = (2ll * c + (begun_here ? 1 : 0)) * Lay::TEAMS + mine;
+          st.put_part(p.part + slot * Lay::slot_floats + member * Lay::image, heads, lane);
         }
       }
       st.clear();
@@ -548,45 +613,66 @@ __global__ void __launch_bounds__(NW * 32, 1)
   cp_async_wait<0>();
 }
 
-// Joins the parts of every item that stretches over several CTAs: block c looks
-// at the cut in front of stretch c and, if it is the first cut through its
-// item, joins the item's parts: each team every TEAMS-th, then the teams.
+// Joins the parts of every item that stretches over several CTAs: block (c, k)
+// has item k of the group through which the cut in front of stretch c is the
+// first.  The parts' weights 2^(m_p - max m) come first, then every thread sums
+// its outputs over the parts: independent loads, in the parts' order.
 template <int D, int DV, int MAPS, bool F16>
-__global__ void __launch_bounds__(NW * 32)
+__global__ void __launch_bounds__(kJoinThreads)
     streamkl_paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
   using Lay = PagedLay<D, DV, MAPS>;
-  extern __shared__ __align__(128) uint8_t smem_join[];
-  __shared__ int scratch[NW];
-  float* buf = reinterpret_cast<float*>(smem_join);
-  int* cum = reinterpret_cast<int*>(smem_join + Lay::buf);
-  const int g = p.H / p.HK, blocks = (g + HB - 1) / HB, items = p.HK * blocks;
-  tile_line<Lay::TILE>(p, items, cum, scratch);
-  // The line depends on lens alone; the parts are there once the first kernel
-  // has ended.  Every block waits, so that this kernel does not end before it.
+  extern __shared__ float weight[];  // [parts][MAPS * heads] references, then weights; the same of sums
+  __shared__ float inv[MAPS * HB];
+  const Deal deal(p, Lay::TEAMS, grid);
+  // Every block waits for the first kernel, so that this one does not end before it.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long total = cum[p.B];
-  const int n = static_cast<int>(min(static_cast<long long>(grid), total));
-  const int c = blockIdx.x + 1;
-  if (c >= n) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int team = warp / Lay::WPT, member = warp % Lay::WPT;
-  const int cut = static_cast<int>(stretch_start(total, c, n));
-  const int before = static_cast<int>(stretch_start(total, c - 1, n));
+  const int c = blockIdx.x + 1, mine = blockIdx.y;
+  const int4 cut = p.cuts[c];  // sequence, group, parts
+  const int parts = cut.z;
+  if (parts == 0 || mine >= deal.hw) return;
   Cursor cur;
-  cur.seek(p, cum, items, blocks, cut);
-  const int start = cut - cur.tile, end = start + cur.ntiles;
-  if (start == cut || start < before) return;  // no item is cut here, or an earlier cut has it
-  State<MAPS, Lay::MT> st;
-  st.clear();
+  cur.group = cut.y;
+  cur.head(deal, mine);
+  const int heads = min(HB, deal.g - cur.first), n = MAPS * heads, vals = Lay::MT * 16 * heads;
   // part 0 ends stretch c - 1, part j > 0 begins stretch c - 1 + j
-  for (int j = team; j == 0 || (c - 1 + j < n && stretch_start(total, c - 1 + j, n) < end); j += Lay::TEAMS) {
-    const long long slot = 2ll * (c - 1 + j) + (j == 0 ? 1 : 0);
-    st.join(p.part + slot * Lay::slot_floats + member * Lay::image, lane);
+  auto part = [&](int j) {
+    return p.part + ((2ll * (c - 1 + j) + (j == 0 ? 1 : 0)) * Lay::TEAMS + mine) * Lay::slot_floats;
+  };
+  float* sums = weight + parts * n;
+  for (int k = threadIdx.x; k < parts * n; k += blockDim.x) {
+    const float2 ml = *reinterpret_cast<const float2*>(part(k / n) + MAPS * vals + (k % n) * 2);
+    weight[k] = ml.x;
+    sums[k] = ml.y;
   }
-  join_warps<Lay>(st, buf, warp, lane);
-  if (team != 0) return;
-  const int hk = cur.hk, first = cur.first;
-  st.template finish<F16>(p, cur.b, hk * g + first, min(HB, g - first), member * Lay::DVW, lane);
+  __syncthreads();
+  if (static_cast<int>(threadIdx.x) < n) {
+    float top = -INFINITY, sum = 0.f;
+    for (int k = threadIdx.x; k < parts * n; k += n) top = fmaxf(top, weight[k]);
+    for (int k = threadIdx.x; k < parts * n; k += n) {
+      const float w = weight[k] == -INFINITY ? 0.f : ex2(weight[k] - top);  // a part that saw nothing
+      weight[k] = w;
+      sum = fmaf(sums[k], w, sum);
+    }
+    inv[threadIdx.x] = sum > 0.f ? 1.f / sum : 0.f;
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < Lay::WPT * vals; k += blockDim.x) {
+    const int member = k / vals, e = k - member * vals;
+    const int h = e / 8 % heads, col = member * Lay::DVW + e / (8 * heads) * 8 + e % 8;
+    float acc[MAPS] = {};
+#pragma unroll 8
+    for (int j = 0; j < parts; ++j) {
+      const float* src = part(j) + member * Lay::image + e;
+#pragma unroll
+      for (int t = 0; t < MAPS; ++t) acc[t] = fmaf(src[t * vals], weight[j * n + t * heads + h], acc[t]);
+    }
+    const int head = cur.hk * deal.g + cur.first + h;
+    float x = acc[0] * inv[h];
+    if (MAPS == 2)
+      x = fmaf(-load_lam(p.lam, cut.x, head, 0, F16), acc[MAPS - 1] * inv[(MAPS - 1) * heads + h], x);
+    static_cast<uint16_t*>(p.O)[cut.x * p.o_b + head * p.o_h + col] =
+        static_cast<uint16_t>(pack2<F16>(x, 0.f));
+  }
 }
 
 template <int D, int DV, int MAPS, bool F16>
@@ -604,9 +690,9 @@ cudaError_t launch_t(const PagedParams& p, int num_sms, cudaStream_t stream) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(num_sms - 1);
-  cfg.blockDim = dim3(NW * 32);
-  cfg.dynamicSmemBytes = Lay::buf + (p.B + 1) * 4;
+  cfg.gridDim = dim3(num_sms - 1, Lay::TEAMS);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 2 * static_cast<size_t>(num_sms) * MAPS * HB * sizeof(float);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -652,10 +738,14 @@ __global__ void __launch_bounds__(256) streamkl_paged_write_kernel(const __grid_
 }  // namespace
 
 size_t paged_workspace_bytes(int dv, int maps, int num_sms) {
-  // two slots per CTA; a slot holds HB heads' outputs and (m, l) pairs per lane
-  const int wpt = dv > 128 ? 2 : 1, mt = dv / wpt / 16;
-  return static_cast<size_t>(2 * num_sms) * wpt * 32 * (maps * mt * 4 + 4 * maps) * 4;
+  // the cuts, then two stretch ends per CTA, a state of every warp: HB heads'
+  // outputs and (m, l)
+  const int mt = (dv > 128 ? 128 : dv) / 16;
+  return paged_cuts_bytes(num_sms) +
+         static_cast<size_t>(2 * num_sms) * NW * (32 * maps * mt * 4 + 2 * maps * HB) * 4;
 }
+
+size_t paged_cuts_bytes(int num_sms) { return (static_cast<size_t>(num_sms) * sizeof(int4) + 255) / 256 * 256; }
 
 cudaError_t launch_paged(const PagedParams& p, int d, int dv, bool f16, int num_sms,
                          cudaStream_t stream) {
