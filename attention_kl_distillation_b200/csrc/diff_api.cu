@@ -110,7 +110,7 @@ streamkl_status check_paged(const streamkl_paged_problem* pr) {
     return STREAMKL_EINVAL;
   if (pr->lam_fp32 & ~1) return STREAMKL_EINVAL;
   if (!std::isfinite(pr->s1) || !std::isfinite(pr->s2)) return STREAMKL_EINVAL;
-  if (pr->B > 4096) return STREAMKL_EINVAL;
+  if (pr->B > 2048) return STREAMKL_EINVAL;
   const int64_t most = static_cast<int64_t>(pr->max_pages) * pr->page_size;
   if (most > (1 << 30)) return STREAMKL_EINVAL;
   // Tiles are counted in int.  One holds 64 tokens of a work item (a key head, 8 of its
@@ -391,6 +391,7 @@ streamkl_status streamkl_paged_write(int n, const streamkl_tensor* rows,
                                      int page_size, streamkl_stream_t stream) {
   if (n < 1 || n > skl::kPagedWriteMax || !rows || !caches || !widths) return STREAMKL_EINVAL;
   if (T < 1 || HK < 1 || pages < 1 || page_size < 1 || (slots_int64 & ~1)) return STREAMKL_EINVAL;
+  if (static_cast<int64_t>(pages) * page_size > UINT32_MAX) return STREAMKL_EINVAL;
   if (!slots || !aligned(slots, slots_int64 ? 8 : 4)) return STREAMKL_EINVAL;
   skl::PagedWriteParams p;
   for (int k = 0; k < n; ++k) {

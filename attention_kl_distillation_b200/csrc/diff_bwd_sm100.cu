@@ -714,7 +714,8 @@ template <int PASS, int D, int DV, int SEL, bool F16>
 cudaError_t launch_t(const DiffBwdParams& p, int num_sms, cudaStream_t stream) {
   using Lay = BwdLay<PASS, D, DV, SEL>;
   auto kern = streamkl_diff_bwd_kernel<PASS, D, DV, SEL, F16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::alloc);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(kern, Lay::alloc, ready);
   if (e != cudaSuccess) return e;
   const int nrows = PASS == kDiffKV ? p.s.NK : p.s.NQ;
   const int units = p.s.B * (PASS == kDiffKV ? p.s.HK : p.s.H) * ((nrows + R - 1) / R) * p.nhalf;

@@ -543,7 +543,8 @@ template <int D, int DVH, bool F16>
 cudaError_t launch_t(const DiffFwdParams& p, int num_sms, cudaStream_t stream) {
   constexpr int smem = FwdLay<D>::alloc;
   auto kern = streamkl_diff_fwd_kernel<D, DVH, F16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(kern, smem, ready);
   if (e != cudaSuccess) return e;
   const int units = p.s.B * p.s.H * ((p.s.NQ + R - 1) / R) * p.nhalf;
   const int grid = units < num_sms ? units : num_sms;

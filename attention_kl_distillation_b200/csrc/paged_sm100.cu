@@ -35,7 +35,7 @@ namespace {
 constexpr int KT = 16;       // keys per team and tile
 constexpr int NW = 8;        // warps per CTA
 constexpr int HB = 8;        // query heads per work item (mma N)
-constexpr int kMaxBatch = 4096;
+constexpr int kMaxBatch = 2048;
 constexpr int kJoinThreads = 512;
 constexpr int kBehind = -2147483647 - 1;
 constexpr float kSlack = 8.f;  // a reference grows only by more than this (log2)
@@ -60,7 +60,8 @@ struct PagedLay {
   static constexpr int cum_off = mask_off + NST * TEAMS * 4;
   static constexpr int alloc(int B) { return cum_off + (B + 1) * 4; }
   static_assert(NST >= 2, "ring too shallow");
-  static_assert(cum_off + (kMaxBatch + 1) * 4 <= 232448, "shared memory budget exceeded");
+  static_assert(alloc(kMaxBatch) + 1024 <= 232448,  // 1 KB: the statically sized part
+                "shared memory budget exceeded");
   // Workspace of one stretch end and team: outputs and (m, l) per map and head, in
   // the fragment order of its warps.
   static constexpr int image = 32 * NREG + 2 * MAPS * HB;  // floats of one warp's part, 8 heads
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             }
           }
       }
-      uint32_t pf[MAPS][2];
+      uint32_t pf[MAPS][2], pr[MAPS][2];
 #pragma unroll
       for (int m = 0; m < MAPS; ++m) {
         const float cm = m ? p.c2 : p.c1;
@@ -562,9 +563,18 @@ __global__ void __launch_bounds__(NW * 32, 1)
           x[m][e] = ex2(fmaf(x[m][e], cm, -ref));
           st.l[m][e & 1] += x[m][e];
         }
-        // P^T as the B operand: heads on rows after the transposition
-        pf[m][0] = transpose8x8(pack2<F16>(x[m][0], x[m][1]));
-        pf[m][1] = transpose8x8(pack2<F16>(x[m][2], x[m][3]));
+        // P^T as the B operand: heads on rows after the transposition.  P goes in as
+        // two 16-bit factors, its rounded value and what the rounding left, so that
+        // the outputs are as exact as fp32 weights would make them; the kernel is
+        // bound by HBM and pays 0 to 2% for the second product (B32 H16 d64/128:
+        // 101 -> 103 us).
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t w = pack2<F16>(x[m][2 * e], x[m][2 * e + 1]);
+          const float2 back = unpack2<F16>(w);
+          pf[m][e] = transpose8x8(w);
+          pr[m][e] = transpose8x8(pack2<F16>(x[m][2 * e] - back.x, x[m][2 * e + 1] - back.y));
+        }
       }
 #pragma unroll
       for (int q = 0; q < MT; ++q) {
@@ -573,7 +583,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     (member * (Lay::DVW / 64) + (q >> 2)) * CHUNK,
                 vf);
 #pragma unroll
-        for (int m = 0; m < MAPS; ++m) mma16816<F16>(st.o[m][q], vf, pf[m][0], pf[m][1]);
+        for (int m = 0; m < MAPS; ++m) {
+          mma16816<F16>(st.o[m][q], vf, pf[m][0], pf[m][1]);
+          mma16816<F16>(st.o[m][q], vf, pr[m][0], pr[m][1]);
+        }
       }
     }
     if (++s == NST) s = 0;
@@ -680,7 +693,8 @@ cudaError_t launch_t(const PagedParams& p, int num_sms, cudaStream_t stream) {
   using Lay = PagedLay<D, DV, MAPS>;
   auto kern = streamkl_paged_kernel<D, DV, MAPS, F16>;
   const int smem = Lay::alloc(p.B);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(kern, Lay::alloc(kMaxBatch), ready);
   if (e != cudaSuccess) return e;
   kern<<<num_sms, NW * 32, smem, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -708,30 +722,46 @@ cudaError_t launch_dims(const PagedParams& p, int d, int dv, int num_sms, cudaSt
   return cudaErrorInvalidValue;
 }
 
-// New rows into their slots, 16 bytes a thread and step; bound by HBM.  A
-// negative slot is skipped (a padded row); one past the cache is skipped and
-// reported.
+// New rows into their slots, 16 bytes a thread and step, STEPS steps' loads in
+// flight: four where that still fills the device (a batch of prompts, 8 heads, d128/256:
+// 33 us against 35), one for a served batch's single tokens, which are bound by
+// latency (64 rows of 16 heads, d64/128: 2.2 us against 3.4).  A negative slot is skipped (a padded row); one past the
+// cache is skipped and reported.
+template <int STEPS>
 __global__ void __launch_bounds__(256) streamkl_paged_write_kernel(const __grid_constant__ PagedWriteParams p) {
   const int w = blockIdx.y;
   const int vecs = p.vecs[w], per = p.HK * vecs;
   const long long total = static_cast<long long>(p.T) * per;
   const long long slots = static_cast<long long>(p.pages) * p.page_size;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const int t = static_cast<int>(i / per), r = static_cast<int>(i - static_cast<long long>(t) * per);
-    const int h = r / vecs, v = r - h * vecs;
-    const long long slot = p.slots64 ? static_cast<const long long*>(p.slots)[t]
-                                     : static_cast<const int*>(p.slots)[t];
-    if (slot < 0) continue;
-    if (slot >= slots) {
-      atomicCAS(p.status, 0, static_cast<int>(STREAMKL_EDEVICE));
-      continue;
+  constexpr int kBlock = 256 * STEPS;
+  for (long long base = static_cast<long long>(blockIdx.x) * kBlock; base < total;
+       base += static_cast<long long>(gridDim.x) * kBlock) {
+    const int t0 = static_cast<int>(base / per), r0 = static_cast<int>(base - static_cast<long long>(t0) * per);
+    uint4 x[STEPS];
+    uint8_t* dst[STEPS];
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      dst[k] = nullptr;
+      const int i = r0 + k * 256 + static_cast<int>(threadIdx.x);  // piece, counted from token t0
+      const int dt = i / per, r = i - dt * per, h = r / vecs, v = r - h * vecs, t = t0 + dt;
+      if (t >= p.T) continue;
+      const long long slot = p.slots64 ? static_cast<const long long*>(p.slots)[t]
+                                       : static_cast<const int*>(p.slots)[t];
+      if (slot < 0) continue;
+      if (slot >= slots) {
+        atomicCAS(p.status, 0, static_cast<int>(STREAMKL_EDEVICE));
+        continue;
+      }
+      // slots of the cache fit in 32 bits: pages * page_size does
+      const unsigned page = static_cast<unsigned>(slot) / static_cast<unsigned>(p.page_size);
+      const unsigned row = static_cast<unsigned>(slot) - page * static_cast<unsigned>(p.page_size);
+      x[k] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.rows[w]) +
+                                             t * p.row_t[w] + h * p.row_h[w] + v * 16);
+      dst[k] = static_cast<uint8_t*>(p.caches[w]) + page * p.page[w] + row * p.slot[w] + h * p.head[w] + v * 16;
     }
-    const long long page = slot / p.page_size, row = slot - page * p.page_size;
-    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.rows[w]) +
-                                                    t * p.row_t[w] + h * p.row_h[w] + v * 16);
-    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.caches[w]) + page * p.page[w] +
-                              row * p.slot[w] + h * p.head[w] + v * 16) = x;
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k)
+      if (dst[k]) *reinterpret_cast<uint4*>(dst[k]) = x[k];
   }
 }
 
@@ -759,10 +789,12 @@ cudaError_t launch_paged(const PagedParams& p, int d, int dv, bool f16, int num_
 cudaError_t launch_paged_write(const PagedWriteParams& p, int num_sms, cudaStream_t stream) {
   int most = 0;
   for (int i = 0; i < p.n; ++i) most = p.vecs[i] > most ? p.vecs[i] : most;
-  const long long blocks = (static_cast<long long>(p.T) * p.HK * most + 255) / 256;
-  const long long cap = 8ll * num_sms;
+  const long long pieces = static_cast<long long>(p.T) * p.HK * most, cap = 8ll * num_sms;
+  const int per = pieces >= 256 * 4 * cap ? 256 * 4 : 256;
+  const long long blocks = (pieces + per - 1) / per;
   const dim3 grid(static_cast<unsigned>(blocks < cap ? blocks : cap), static_cast<unsigned>(p.n));
-  streamkl_paged_write_kernel<<<grid, 256, 0, stream>>>(p);
+  if (per == 256) streamkl_paged_write_kernel<1><<<grid, 256, 0, stream>>>(p);
+  else streamkl_paged_write_kernel<4><<<grid, 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

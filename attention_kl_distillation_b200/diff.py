@@ -67,28 +67,23 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _Meta = namedtuple("_Meta", "shape stride dtype device")
 
 
-def _key(t):
-    """What a check of t depends on, as it comes; None for None."""
-    if t is None:
-        return None
+def _keys(*tensors):
+    """What the checks depend on, as it comes; None for None."""
     try:
-        return t.shape, t.stride(), t.dtype, t.device
+        return [None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in tensors]
     except AttributeError:
         raise ValueError("operands must be tensors") from None
 
 
 def _meta(t):
     """The same with names."""
-    return _Meta(*_key(t)) if t is not None else None
+    return _Meta(*_keys(t)[0]) if t is not None else None
 
 
 def _planned(plan):
     """A plan class as a function of keys: each key becomes a _Meta, the result is kept."""
-    def named(k):
-        if isinstance(k, tuple):
-            return _Meta(*k) if len(k) == 4 and isinstance(k[2], torch.dtype) else tuple(map(named, k))
-        return k
-    return functools.lru_cache(maxsize=512)(lambda *keys: plan(*map(named, keys)))
+    return functools.lru_cache(maxsize=512)(
+        lambda *keys: plan(*(_Meta(*k) if isinstance(k, tuple) else k for k in keys)))
 
 
 def _contiguous(m) -> bool:
@@ -180,7 +175,7 @@ def _scale(s):
 
 class _Structs:
     """streamkl_tensor structs without their pointers; ``at`` puts the pointers in, in a new copy, and
-    gives the addresses to pass.  Entries of None stay NULL."""
+    gives the addresses to pass, NULL for a pointer of 0."""
 
     def __init__(self, strides):
         words = []
@@ -191,15 +186,9 @@ class _Structs:
 
     def at(self, pointers):
         block = self.type.from_buffer_copy(self.template)
+        block[::4] = pointers
         base = ctypes.addressof(block)
-        out = []
-        for k, p in enumerate(pointers):
-            if p is None:
-                out.append(None)
-            else:
-                block[4 * k] = p
-                out.append(base + 32 * k)
-        return block, out
+        return block, [base + 32 * k if p else None for k, p in enumerate(pointers)]
 
 
 def _outer(m):
@@ -231,11 +220,11 @@ def _like(m, width):
 
 
 def _pointers(*tensors):
-    """Data pointers, None for None; operands start on 16 bytes."""
-    out = [None if t is None else t.data_ptr() for t in tensors]
+    """Data pointers, 0 for None; operands start on 16 bytes."""
+    out = [0 if t is None else t.data_ptr() for t in tensors]
     low = 0
     for p in out:
-        low |= p or 0
+        low |= p
     if low & 15:
         raise ValueError("operands must be 16-byte aligned")
     return out
@@ -256,12 +245,12 @@ def _run(fn, where, device, *args):
         raise StreamKLError(st, where)
 
 
-def _workspace(ws, need, device):
+def _workspace(ws, need, like):
     """The caller's workspace, or one from the caching allocator: (tensor, pointer, bytes)."""
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = like.new_empty(need, dtype=torch.uint8)
         return ws, ws.data_ptr(), need
-    if not isinstance(ws, torch.Tensor) or ws.device != device or not ws.is_contiguous():
+    if not isinstance(ws, torch.Tensor) or ws.device != like.device or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     have = ws.numel() * ws.element_size()
     if have < need:
@@ -298,7 +287,8 @@ class _DiffPlan:
         self.device, self.dtype = Q1.device, Q1.dtype
         self.rows, self.out, self.q = (B, H, NQ), (B, H, NQ, dv), Q1
         self.empty = 0 in self.out or HK == 0
-        self.mO = None  # an output's layout, once there has been one
+        self.out_shape, self.out_back = _like_shape(Q1.shape, Q1.stride, dv)
+        self.fwd = {}   # the forward's C structs for outputs in Q1's memory order, with and without O2
         self.no_keys = NK == 0
         self.prob = diff_problem(B, H, HK, NQ, NK, d, dv, causal, s1, s2, Q1.dtype, lam.dtype == torch.float32)
         self.prob_at = ctypes.addressof(self.prob)
@@ -310,11 +300,9 @@ _diff_plan = _planned(_DiffPlan)
 
 
 def _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2):
-    return _diff_plan(_key(Q1), _key(K1), _key(Q2), _key(K2), _key(V), _key(lam), _key(q_lens),
-                      _key(k_lens), bool(causal), s1, s2)
+    return _diff_plan(*_keys(Q1, K1, Q2, K2, V, lam, q_lens, k_lens), bool(causal), s1, s2)
 
 
-@functools.lru_cache(maxsize=512)
 def _fwd_structs(plan, O, O2):
     return _Structs([*plan.inputs, _outer(O), _outer(O2) if O2 is not None else None])
 
@@ -334,13 +322,13 @@ def diff_attn_fwd(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens
     lam = _lam(lam)
     plan = _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2)
     if out is None:
-        O = _like(plan.q, plan.out[3])
-        if plan.mO is None:
-            plan.mO = _meta(O)
-        O2 = torch.empty_like(O) if save else None
-        LSE1, LSE2 = (torch.empty(plan.rows, dtype=torch.float32, device=plan.device)
-                      if save else None for _ in range(2))
-        mO, mO2 = plan.mO, plan.mO if save else None
+        O, O2 = (Q1.new_empty(plan.out_shape) if k == 0 or save else None for k in range(2))
+        if plan.out_back is not None:
+            O, O2 = O.permute(plan.out_back), O2.permute(plan.out_back) if save else None
+        LSE1, LSE2 = (Q1.new_empty(plan.rows, dtype=torch.float32) if save else None for _ in range(2))
+        structs = plan.fwd.get(save)
+        if structs is None:
+            structs = plan.fwd[save] = _fwd_structs(plan, _meta(O), _meta(O2))
     else:
         out = tuple(out)
         if len(out) != 4:
@@ -353,13 +341,14 @@ def diff_attn_fwd(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens
             _check_same_strides(mO, mO2)
             _check_rows("LSE1", _meta(LSE1), plan.rows, plan.q)
             _check_rows("LSE2", _meta(LSE2), plan.rows, plan.q)
+        structs = _fwd_structs(plan, mO, mO2)
     if plan.empty or plan.no_keys:
         for t, v in ((O, 0.0), (O2, 0.0), (LSE1, -float("inf")), (LSE2, -float("inf"))):
             if t is not None:
                 t.fill_(v)
         return O, O2, LSE1, LSE2
     p = _pointers(Q1, K1, Q2, K2, V, O, O2)
-    block, at = _fwd_structs(plan, mO, mO2).at([*p[:5], lam.data_ptr(), *p[5:]])
+    block, at = structs.at([*p[:5], lam.data_ptr(), *p[5:]])
     _run(_lib.streamkl_diff_fwd, "streamkl_diff_fwd", plan.device, plan.prob_at, *at[:6], _ptr(q_lens),
          _ptr(k_lens), *at[6:], _ptr(LSE1), _ptr(LSE2))
     return O, O2, LSE1, LSE2
@@ -423,7 +412,7 @@ def diff_attn_bwd(dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, causal=False, s
         return tuple(outs)
     p = _pointers(dO, *inputs, O, O2, *outs[:5])
     block, at = structs.at([*p[:6], lam.data_ptr(), *p[6:]])
-    ws, ws_at, ws_bytes = _workspace(workspace, plan.ws_bytes, plan.device)
+    ws, ws_at, ws_bytes = _workspace(workspace, plan.ws_bytes, Q1)
     _run(_lib.streamkl_diff_bwd, "streamkl_diff_bwd", plan.device, plan.prob_at, *at[:9], _ptr(LSE1),
          _ptr(LSE2), _ptr(q_lens), _ptr(k_lens), *at[9:], _ptr(outs[5]), ws_at, ws_bytes)
     return tuple(outs)
@@ -454,8 +443,7 @@ def diff_attn(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens=Non
 
     Arguments as in ``diff_attn_fwd``.  O's axes are in Q1's memory order.  Where no gradient is
     wanted, nothing is saved."""
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad
-                                       for t in (Q1, K1, Q2, K2, V, lam)):
+    if torch.is_grad_enabled() and any([getattr(t, "requires_grad", False) for t in (Q1, K1, Q2, K2, V, lam)]):
         return _DiffAttnFunction.apply(Q1, K1, Q2, K2, V, lam, causal, s1, s2, q_lens, k_lens)
     return diff_attn_fwd(Q1, K1, Q2, K2, V, lam, causal, s1, s2, q_lens, k_lens, save=False)[0]
 
@@ -515,15 +503,14 @@ _paged_plan = _planned(_PagedPlan)
 
 def _paged(Q1, K1, Q2, K2, V, lam, table, lens, s1, s2, workspace, out):
     lam = _lam(lam)
-    plan = _paged_plan(_key(Q1), _key(K1), _key(Q2), _key(K2), _key(V), _key(lam), _key(table),
-                       _key(lens), _key(out), s1, s2)
+    plan = _paged_plan(*_keys(Q1, K1, Q2, K2, V, lam, table, lens, out), s1, s2)
     if out is None:
-        out = torch.empty(plan.out, dtype=plan.dtype, device=plan.device)
+        out = Q1.new_empty(plan.out)
     if plan.empty or plan.no_keys:
         return out.zero_()
     p = _pointers(Q1, K1, Q2, K2, V, out)
-    block, at = plan.structs.at([*p[:5], _ptr(lam), p[5]])
-    ws, ws_at, ws_bytes = _workspace(workspace, plan.ws_bytes, plan.device)
+    block, at = plan.structs.at([*p[:5], lam.data_ptr() if lam is not None else 0, p[5]])
+    ws, ws_at, ws_bytes = _workspace(workspace, plan.ws_bytes, Q1)
     _run(_lib.streamkl_paged_attn, "streamkl_paged_attn", plan.device, plan.prob_at, *at[:6],
          table.data_ptr(), plan.table_stride, lens.data_ptr(), at[6], ws_at, ws_bytes)
     return out
@@ -564,7 +551,8 @@ def paged_workspace_size(dv, maps, device=None) -> int:
 class _WritePlan:
     """One write's checked dimensions and C structs."""
 
-    def __init__(self, rows, caches, slots):
+    def __init__(self, n, *metas):
+        rows, caches, slots = metas[:n], metas[n:-1], metas[-1]
         first = rows[0]
         if first is None or len(first.shape) != 3:
             raise ValueError("rows[0] must be a tensor [T, HK, width]")
@@ -604,11 +592,10 @@ def paged_write(rows, caches, slots):
     [pages, page_size, HK, width], row t into slot slots[t] = page * page_size + row of the page
     (int32 or int64 [T]).  A negative slot is skipped, one past the cache is skipped and recorded for
     ``query_device_status``.  Slots must be distinct; the rest of the caches stays as it was."""
-    rows, caches = tuple(rows), tuple(caches)
     n = len(rows)
     if not 1 <= n <= 4 or n != len(caches):
         raise ValueError("rows and caches must be tuples of the same length, one to four")
-    plan = _write_plan(tuple(map(_key, rows)), tuple(map(_key, caches)), _key(slots))
+    plan = _write_plan(n, *_keys(*rows, *caches, slots))
     if plan.empty:
         return
     block, at = plan.structs.at(_pointers(*rows, *caches))

@@ -360,7 +360,7 @@ streamkl_status streamkl_diff_bwd(const streamkl_diff_problem *prob, const strea
  * table behind a sequence's length are not read.  An entry outside 0..pages-1
  * is not followed: its tokens are left out.  Both that and a length past the
  * table make streamkl_query_device_status return STREAMKL_EDEVICE.
- * 1 <= B <= 4096, pages, page_size, max_pages >= 1.
+ * 1 <= B <= 2048, pages, page_size, max_pages >= 1.
  */
 typedef struct {
   int B, H, HK, d, dv, dtype, lam_fp32, pages, page_size, max_pages;

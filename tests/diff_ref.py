@@ -5,6 +5,7 @@ Bounds (per element, worst case; u = half a step of the inputs' 16-bit type, rel
   P_t   relative error c: the scores' fp32 sums of d products (an absolute error of x is a relative
         one of exp x), the fp32 sum of the row, the hardware exponential (2^-22)
   O     u of the result; u + c of each p V, because P is rounded to 16 bits for its product
+        (paged forms: u^2, the rounded value's remainder goes in as a second factor)
   D_t   sum |dO| (error of O_t, which is read back in 16 bits)
   X1    P1 (G - D1): u + c of the value, P1 times the errors of G and D1;  X2 alike
   dQ, dK, dV  the error of the 16-bit factor times the other factor's size, u of the result
@@ -49,7 +50,8 @@ def lam_rows(lam, B, H, NQ):
 class Reference:
     """Everything about one problem, in 64 bits; rows outside the lengths count as zero."""
 
-    def __init__(self, Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens=None, k_lens=None):
+    def __init__(self, Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens=None, k_lens=None,
+                 factors=1):
         self.dtype, dev = Q1.dtype, Q1.device
         B, H, NQ, d = Q1.shape
         HK, NK = K1.shape[1:3]
@@ -88,7 +90,7 @@ class Reference:
         self.u, self.t = u, t
         size = [P @ self.V.abs() for P in self.P]
         low = (t + FLUSH) * (seen.double() @ self.V.abs())
-        self.dO_t = [(u + self.c) * z + low for z in size]   # unrounded outputs
+        self.dO_t = [(u ** factors + self.c) * z + low for z in size]   # unrounded outputs
         self.tol_O = (self.dO_t[0] + self.lam.abs() * self.dO_t[1]) * (1 + u) + u * self.O.abs() + t
         self.tol_O2 = self.dO_t[1] * (1 + u) + u * self.O_t[1].abs() + t
         self.tol_LSE = self.c + 2.0 ** -21 * max([1.0] + [float(l[torch.isfinite(l)].abs().max())
@@ -165,6 +167,6 @@ def paged_reference(Q1, K1, Q2, K2, V, lam, table, lens, s1=None, s2=None):
                       (Q2 if two else Q1)[b].view(1, H, 1, d), pages_of(K2 if two else K1, table, b, n)[None],
                       pages_of(V, table, b, n)[None],
                       (lam if lam.dim() < 2 else lam.expand(B, H)[b]) if two else torch.zeros((), device=Q1.device),
-                      False, s1, s2)
+                      False, s1, s2, factors=2)
         out[b], tol[b] = r.O[0, :, 0], r.tol_O[0, :, 0]
     return out, tol

@@ -187,8 +187,8 @@ def test_paged_abi_refuses():
         a.update(bad)
         return B.lib().streamkl_paged_attn(ctypes.byref(D.PagedProblem(*p.values())), *a.values(), None)
 
-    for bad in (dict(B=0), dict(B=4097), dict(H=0), dict(HK=3), dict(pages=0), dict(page_size=0), dict(max_pages=0),
-                dict(s1=math.nan), dict(max_pages=1 << 28, page_size=16), dict(B=4096, H=4096, HK=4096, max_pages=1 << 16)):
+    for bad in (dict(B=0), dict(B=2049), dict(H=0), dict(HK=3), dict(pages=0), dict(page_size=0), dict(max_pages=0),
+                dict(s1=math.nan), dict(max_pages=1 << 28, page_size=16), dict(B=2048, H=4096, HK=4096, max_pages=1 << 16)):
         assert call(bad) == B.EINVAL, bad
     for bad in (dict(d=64, dv=256), dict(d=32), dict(dtype=5)):
         assert call(bad) == B.EUNSUPPORTED
@@ -205,7 +205,7 @@ def test_write_abi_refuses():
                                             wide, T, HK, pages, page, None)
 
     for bad in (dict(n=0), dict(n=5), dict(T=0), dict(HK=0), dict(pages=0), dict(page=0), dict(width=12), dict(width=0),
-                dict(slots=0), dict(slots=4), dict(wide=2), dict(row=(0, 0, 64, 128)), dict(row=(256, 0, 0, 128)),
+                dict(slots=0), dict(slots=4), dict(wide=2), dict(pages=1 << 20, page=1 << 13), dict(row=(0, 0, 64, 128)), dict(row=(256, 0, 0, 128)),
                 dict(cache=(520, 2048, 64, 128)), dict(cache=(512, 2044, 64, 128))):
         assert call(**bad) == B.EINVAL, bad
 
