@@ -24,9 +24,11 @@
 // With X1 and X2 both there, A goes through shared memory (K-major, 128-byte
 // swizzle); in the dV-only pass it takes X1's place.
 //
-// The issuer's order is  G(t+1)  OUT(t)  S(t+2)  behind "X(t) is written": S of
-// a step and its exponentials, and G, are then under way while the step
-// before is contracted, and one step costs about the sum of its products.
+// Two threads issue.  One gives out S(t+1) as soon as the warps have read S(t),
+// and G(t+1) as soon as they have read G(t); the other the output products of
+// step t once X(t) is written.  S, its exponentials and G are then under way
+// while the step before is contracted, the next unit's begin during this one's
+// end, and one thread's waits are filled with the other's products.
 //
 // TMEM holds 256 output columns beside the 256 above, shared memory the
 // resident tiles and two stages. That decides the passes:
@@ -83,8 +85,8 @@ struct BwdLay {
   static constexpr int rec_off = c_off + NST * stage;
   static constexpr int bar_off = rec_off + NST * rec;
   // cfull cempty craw [NST], vfull vempty vraw [NSV], rfull rempty sfull sempty
-  // gfull xfull xempty ofull oempty drain
-  static constexpr int nbar = 3 * NST + 3 * NSV + 10;
+  // gfull xfull xempty ofull oempty drain[2]
+  static constexpr int nbar = 3 * NST + 3 * NSV + 11;
   static constexpr int misc_off = bar_off + nbar * 8;
   static constexpr int alloc = misc_off + 16 + 1024;
   static constexpr int o1 = kColOut;
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* xempty = xfull + 1;  // ... and have been contracted
   uint64_t* ofull = xempty + 1;
   uint64_t* oempty = ofull + 1;
-  uint64_t* drain = oempty + 1;
+  uint64_t* drain = oempty + 1;  // [2]: the issuers' own products are done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::misc_off);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::misc_off + 4);
 
@@ -247,7 +249,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(xempty, 1);
     mbar_init(ofull, 1);
     mbar_init(oempty, 4 * NWG);
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     fence_mbar_init();
     if (Lay::S1) tma_prefetch_desc(&p.tmR1);
     if (Lay::S2) tma_prefetch_desc(&p.tmR2);
@@ -543,55 +546,32 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               mbar_wait(armed_v[s] > 2 ? &vraw[s] : &vfull[s], (armed_v[s] - 1) & 1u, dctl);
         }
       }
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ UMMA issuer
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ issuer of S and G
       if (lane == 0) {
         constexpr uint32_t idS = idesc_16<F16>(R, CB);
-        constexpr uint32_t idD = idesc_16<F16>(R, D, 0, 1);  // B = C, features contiguous
-        constexpr uint32_t idV = idesc_16<F16>(R, DV, 0, 1);
         const uint64_t r1d = sdesc_sw128(smem_u32(r1_s), 16, 1024);
         const uint64_t r2d = sdesc_sw128(smem_u32(r2_s), 16, 1024);
         const uint64_t r3d = sdesc_sw128(smem_u32(r3_s), 16, 1024);
-        const uint64_t ad = sdesc_sw128(smem_u32(a_s), 16, 1024);
-        int cs = 0, cn = 0;  // stage of the step whose products are next, and of the one after
-        uint32_t rph = 0, cph = 0, seph = 0, xph = 0, oph = 0;
-        bool ok = true;
+        int cn = 0, cg = 0;  // stages of the next S, and of the next G's streamed tile
+        uint32_t rph = 0, cph = 0, vph = 0, seph = 0, xph = 0;
+        bool ok = true, first_s = true, first_g = true;  // of the whole run: nothing was read before
         auto product = [&](uint32_t col, uint64_t resident, uint8_t* tile, int width) {
           const uint64_t rd = here(resident);
           const uint64_t cd = sdesc_sw128(smem_u32(tile), 16, 1024);
-  #pragma unroll
+#pragma unroll
           for (int kk = 0; kk < width / 16; ++kk)
             umma_bf16_ss(tmem + col, sdesc_advance(rd, (kk >> 2) * (R * 128) + (kk & 3) * 32),
                          sdesc_advance(cd, (kk >> 2) * (CB * 128) + (kk & 3) * 32), idS, kk > 0);
         };
-        int gt = 0;  // steps so far: A alternates between two buffers
-        int cg = 0;  // where the next G's streamed tile is
-        uint32_t vph = 0;
-        auto issue_g = [&]() -> bool {
-          if (!Lay::WG) return true;
-          if (!Lay::CR3) {
-            if (!mbar_wait(&vfull[cg], vph, ctl)) return false;
-            tc_fence_after();
-          }
-          product(kColG, r3d, c3_s(cg), DV);
-          umma_commit(gfull);
-          if (!Lay::CR3) umma_commit(&vempty[cg]);
-          if (++cg == (Lay::CR3 ? NST : NSV)) {
-            cg = 0;
-            vph ^= 1;
-          }
-          return true;
-        };
-        // S of the step in stage cn, once its tiles are there and the warps have
-        // read the S before
-        bool first_step = true;  // of the whole run: nothing was read before
+        // S, once its tiles are there and the warps have read the S before
         auto issue_s = [&]() -> bool {
           if (!mbar_wait(&cfull[cn], cph, ctl)) return false;
-          if (!first_step) {
+          if (!first_s) {
             if (!mbar_wait(sempty, seph, ctl)) return false;
             seph ^= 1;
           }
-          first_step = false;
+          first_s = false;
           tc_fence_after();
           if (Lay::S1) product(0, r1d, c1_s(cn), D);
           if (Lay::S2) product(kColS2, r2d, c2_s(cn), D);
@@ -602,6 +582,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           return true;
         };
+        // G, once the warps have read the G before (xfull says that too)
+        auto issue_g = [&]() -> bool {
+          if (!first_g) {
+            if (!mbar_wait(xfull, xph, ctl)) return false;
+            xph ^= 1;
+          }
+          first_g = false;
+          if (!Lay::CR3 && !mbar_wait(&vfull[cg], vph, ctl)) return false;
+          tc_fence_after();
+          product(kColG, r3d, c3_s(cg), DV);
+          umma_commit(gfull);
+          if (!Lay::CR3) umma_commit(&vempty[cg]);
+          if (++cg == (Lay::CR3 ? NST : NSV)) {
+            cg = 0;
+            vph ^= 1;
+          }
+          return true;
+        };
         while (ok && sched.next(u)) {
           const BwdUnit w = decode<PASS>(p, u);
           if (w.tiles == 0) continue;
@@ -609,27 +607,48 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           rph ^= 1;
           const int steps = w.heads * w.tiles;
           if (!(ok = issue_s())) break;
-          ok = issue_g();
-          if (!ok) break;
-          if (steps > 1) {
-            if (!(ok = issue_s())) break;
-          }
           for (int t = 0; t < steps; ++t) {
-            if (!(ok = mbar_wait(xfull, xph, ctl))) break;
-            xph ^= 1;
-            tc_fence_after();
-            if (t + 1 < steps) {
+            if (Lay::WG) {
               ok = issue_g();
               if (!ok) break;
             }
+            if (t + 1 < steps) {
+              ok = issue_s();
+              if (!ok) break;
+            }
+          }
+          if (!ok) break;
+          umma_commit(rempty);
+        }
+        umma_commit(&drain[1]);
+        volatile int zero = 0;
+        WaitCtl dctl{&zero, p.status, p.wait_limit_ns};
+        mbar_wait(&drain[1], 0, dctl);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ issuer of the output products
+      if (lane == 0) {
+        constexpr uint32_t idD = idesc_16<F16>(R, D, 0, 1);  // B = C, features contiguous
+        constexpr uint32_t idV = idesc_16<F16>(R, DV, 0, 1);
+        const uint64_t ad = sdesc_sw128(smem_u32(a_s), 16, 1024);
+        int cs = 0, gt = 0;  // stage, and steps so far: A alternates between two buffers
+        uint32_t xph = 0, oph = 0;
+        bool ok = true;
+        while (ok && sched.next(u)) {
+          const BwdUnit w = decode<PASS>(p, u);
+          if (w.tiles == 0) continue;
+          const int steps = w.heads * w.tiles;
+          for (int t = 0; t < steps; ++t) {
+            if (!(ok = mbar_wait(xfull, xph, ctl))) break;
+            xph ^= 1;
             if (t == 0) {
               if (!(ok = mbar_wait(oempty, oph ^ 1, ctl))) break;
               oph ^= 1;
-              tc_fence_after();
             }
+            tc_fence_after();
             const uint64_t c1m = sdesc_sw128(smem_u32(c1_s(cs)), CB * 128, 1024);
             const uint64_t c2m = sdesc_sw128(smem_u32(c2_s(cs)), CB * 128, 1024);
-            const uint64_t c3m = sdesc_sw128(smem_u32(c3_s(cs)), CB * 128, 1024);
+            const uint64_t c3m = sdesc_sw128(smem_u32(c3_s(Lay::CR3 ? cs : 0)), CB * 128, 1024);
             const uint64_t a_d = sdesc_advance(here(ad), (gt & 1) * (R * CB * 2));
 #pragma unroll
             for (int kk = 0; kk < CB / 16; ++kk) {
@@ -643,22 +662,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               else if (Lay::WV)
                 umma_bf16_ts(tmem + Lay::o3, tmem + kColX1 + kk * 8, sdesc_advance(c3m, kk * 2048), idV, acc);
             }
+            // S and G of this step were complete before X was formed from them, so
+            // this commit also says that nothing reads the stage any more
             umma_commit(&cempty[cs]);
             umma_commit(xempty);
             ++gt;
             if (++cs == NST) cs = 0;
-            if (t + 2 < steps) {
-              if (!(ok = issue_s())) break;
-            }
           }
           if (!ok) break;
           umma_commit(ofull);
-          umma_commit(rempty);
         }
-        umma_commit(drain);
+        umma_commit(&drain[0]);
         volatile int zero = 0;
         WaitCtl dctl{&zero, p.status, p.wait_limit_ns};
-        mbar_wait(drain, 0, dctl);
+        mbar_wait(&drain[0], 0, dctl);
       }
     } else if (warp == 2) {
       // ------------------------------------------------------------ ragged tiles
