@@ -296,38 +296,39 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       iph ^= 1;
       tc_fence_after();
       const float i1 = inv_s[row], i2 = inv_s[R + row];
+      // all of this thread's columns at once: the row's products are no longer held
       const uint32_t c1 = tl + kColO + t * CW, c2 = c1 + 128;
+      uint32_t a[CW], b[CW];
 #pragma unroll
-      for (int e = 0; e < CW; e += 16) {
-        uint32_t a[16], b[16];
-        tmem_ld_32x32b_x16(c1 + e, a);
-        tmem_ld_32x32b_x16(c2 + e, b);
-        tmem_ld_wait();
-        reg_fence(a);
-        reg_fence(b);
-        uint32_t x[8], y[8];
+      for (int e = 0; e < CW; e += 32) {
+        tmem_ld_32x32b_x32(c1 + e, reinterpret_cast<uint32_t(&)[32]>(a[e]));
+        tmem_ld_32x32b_x32(c2 + e, reinterpret_cast<uint32_t(&)[32]>(b[e]));
+      }
+      tmem_ld_wait();
+      reg_fence(a);
+      reg_fence(b);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(oempty);  // the next unit's value products may begin
+      // rows without a visible key are 0 whatever the accumulators hold
+      const bool live = i1 != 0.f && row_ok;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          // rows without a visible key are 0 whatever the accumulators hold
-          const float a0 = i1 != 0.f ? __uint_as_float(a[2 * k]) * i1 : 0.f;
-          const float a1 = i1 != 0.f ? __uint_as_float(a[2 * k + 1]) * i1 : 0.f;
-          const float b0 = i2 != 0.f ? __uint_as_float(b[2 * k]) * i2 : 0.f;
-          const float b1 = i2 != 0.f ? __uint_as_float(b[2 * k + 1]) * i2 : 0.f;
-          x[k] = i1 != 0.f ? pack2<F16>(fmaf(-lam, b0, a0), fmaf(-lam, b1, a1)) : 0u;
-          y[k] = pack2<F16>(b0, b1);
+      for (int e = 0; e < CW; e += 8) {
+        uint32_t x[4], y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // both maps' outputs are rounded alike, so that equal maps cancel exactly
+          const float b0 = __uint_as_float(b[e + 2 * k]) * i2, b1 = __uint_as_float(b[e + 2 * k + 1]) * i2;
+          x[k] = live ? pack2<F16>(fmaf(-lam, b0, __uint_as_float(a[e + 2 * k]) * i1),
+                                   fmaf(-lam, b1, __uint_as_float(a[e + 2 * k + 1]) * i1))
+                      : 0u;
+          y[k] = live ? pack2<F16>(b0, b1) : 0u;
         }
         if (row_ok) {
           *reinterpret_cast<uint4*>(orow + e) = make_uint4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<uint4*>(orow + e + 8) = make_uint4(x[4], x[5], x[6], x[7]);
-          if (o2row) {
-            *reinterpret_cast<uint4*>(o2row + e) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(o2row + e + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-          }
+          if (o2row) *reinterpret_cast<uint4*>(o2row + e) = make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(oempty);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
