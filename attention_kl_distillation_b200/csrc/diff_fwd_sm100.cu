@@ -32,6 +32,8 @@
 // round trip of O through registers.
 #include "diff_sm100.cuh"
 
+#include <type_traits>
+
 namespace skl {
 namespace {
 
@@ -269,17 +271,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           L[(static_cast<long long>(w.b) * p.s.H + w.h) * p.s.NQ + i] =
               seen ? kLn2 * (m + lg2(l)) : -INFINITY;
       }
-      constexpr int CW = DVH / 2;
-      const long long o = w.b * p.o.b + w.h * p.o.h + i * p.o.n + w.half * DVH + t * CW;
-      uint16_t* orow = static_cast<uint16_t*>(p.O) + o;
-      uint16_t* o2row = p.O2 ? static_cast<uint16_t*>(p.O2) + o : nullptr;
+      // Rows are stored NP lanes together (see transpose_pieces): this lane has one
+      // 16-byte piece of each of the NP rows from g0 on.
+      constexpr int CW = DVH / 2, NP = CW / 8;
       const bool row_ok = i < p.s.NQ;
+      const int g0 = w.q0 + quarter * 32 + lane / NP * NP;
+      const long long o0 = w.b * p.o.b + w.h * p.o.h + g0 * p.o.n + w.half * DVH + t * CW + lane % NP * 8;
       if (w.nkt == 0) {
-        if (row_ok) {
 #pragma unroll
-          for (int e = 0; e < CW; e += 8) {
-            *reinterpret_cast<uint4*>(orow + e) = make_uint4(0u, 0u, 0u, 0u);
-            if (o2row) *reinterpret_cast<uint4*>(o2row + e) = make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < NP; ++k) {
+          if (g0 + k < p.s.NQ) {
+            const long long o = o0 + k * p.o.n;
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O) + o) = make_uint4(0u, 0u, 0u, 0u);
+            if (p.O2) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O2) + o) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         continue;
@@ -312,23 +316,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (lane == 0) mbar_arrive(oempty);  // the next unit's value products may begin
       // rows without a visible key are 0 whatever the accumulators hold
       const bool live = i1 != 0.f && row_ok;
+      const float2 I1 = make_float2(i1, i1), I2 = make_float2(i2, i2), NL = make_float2(-lam, -lam);
+      auto pair = [](const uint32_t* v) { return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])); };
+      auto pieces = [&](auto second, void* out) {
+        uint4 x[NP];
 #pragma unroll
-      for (int e = 0; e < CW; e += 8) {
-        uint32_t x[4], y[4];
+        for (int e = 0; e < NP; ++e) {
+          uint32_t v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // both maps' outputs are rounded alike, so that equal maps cancel exactly
-          const float b0 = __uint_as_float(b[e + 2 * k]) * i2, b1 = __uint_as_float(b[e + 2 * k + 1]) * i2;
-          x[k] = live ? pack2<F16>(fmaf(-lam, b0, __uint_as_float(a[e + 2 * k]) * i1),
-                                   fmaf(-lam, b1, __uint_as_float(a[e + 2 * k + 1]) * i1))
-                      : 0u;
-          y[k] = live ? pack2<F16>(b0, b1) : 0u;
+          for (int k = 0; k < 4; ++k) {
+            // both maps' outputs are rounded alike, so that equal maps cancel exactly
+            float2 r = __fmul2_rn(pair(&b[8 * e + 2 * k]), I2);
+            if (!decltype(second)::value) r = __ffma2_rn(r, NL, __fmul2_rn(pair(&a[8 * e + 2 * k]), I1));
+            v[k] = live ? pack2<F16>(r.x, r.y) : 0u;
+          }
+          x[e] = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        if (row_ok) {
-          *reinterpret_cast<uint4*>(orow + e) = make_uint4(x[0], x[1], x[2], x[3]);
-          if (o2row) *reinterpret_cast<uint4*>(o2row + e) = make_uint4(y[0], y[1], y[2], y[3]);
-        }
-      }
+        transpose_pieces<NP>(x, lane);
+        uint16_t* dst = static_cast<uint16_t*>(out) + o0;
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+          if (g0 + k < p.s.NQ) *reinterpret_cast<uint4*>(dst + k * p.o.n) = x[k];
+      };
+      pieces(std::false_type{}, p.O);
+      if (p.O2) pieces(std::true_type{}, p.O2);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");

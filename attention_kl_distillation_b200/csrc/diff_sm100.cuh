@@ -82,6 +82,29 @@ __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int chunks, int ro
   }
 }
 
+// Transposes NP 16-byte pieces among each NP neighbouring lanes: lane i of such
+// a group starts with pieces 0..NP-1 of its own row and ends with piece i of the
+// group's rows 0..NP-1, so that one store of the group covers a row's NP pieces.
+// (Each lane storing its own row touches 32 lines with every instruction.)
+template <int NP>
+__device__ __forceinline__ void transpose_pieces(uint4 (&p)[NP], int lane) {
+#pragma unroll
+  for (int s = 1; s < NP; s <<= 1) {
+    const bool up = (lane & s) != 0;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      if (j & s) continue;
+      uint4 give = up ? p[j] : p[j | s];
+      give.x = __shfl_xor_sync(0xffffffffu, give.x, s);
+      give.y = __shfl_xor_sync(0xffffffffu, give.y, s);
+      give.z = __shfl_xor_sync(0xffffffffu, give.z, s);
+      give.w = __shfl_xor_sync(0xffffffffu, give.w, s);
+      if (up) p[j] = give;
+      else p[j | s] = give;
+    }
+  }
+}
+
 // Units dealt to a persistent grid in a snake order (longest first).
 struct SnakeSched {
   int total, G, cta, round;
