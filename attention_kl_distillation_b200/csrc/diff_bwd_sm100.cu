@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const int t = e ? w.tiles - 1 : 0;
             if (!w.ragged(t, nstream)) continue;
             const int s = static_cast<int>((static_cast<unsigned>(item) + t) % NST), c0 = (w.c_first + t) * CB;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&craw[s], (rawph >> s) & 1u, ctl)))) break;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait_long(&craw[s], (rawph >> s) & 1u, ctl)))) break;
             rawph ^= 1u << s;
             const int lo = max(0, w.lo - c0), hi = min(CB, max(0, w.hi - c0));
             auto clean = [&](uint8_t* tile, int chunks) {
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (lane == 0) mbar_arrive(&cfull[s]);
             if (!Lay::CR3) {
               const int v = static_cast<int>((static_cast<unsigned>(item) + t) % (NSV + Lay::CR3));
-              if (!(ok = __all_sync(0xffffffffu, mbar_wait(&vraw[v], (vrawph >> v) & 1u, ctl)))) break;
+              if (!(ok = __all_sync(0xffffffffu, mbar_wait_long(&vraw[v], (vrawph >> v) & 1u, ctl)))) break;
               vrawph ^= 1u << v;
               clean(c3_s(v), DV / 64);
               fence_proxy_async_smem();

@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         item += w.nkt * Lay::ITEMS;
         if (!w.ragged) continue;
         const int s = static_cast<int>((item - 1) % NS);
-        if (!__all_sync(0xffffffffu, mbar_wait(&raw[s], (rawph >> s) & 1u, ctl))) break;
+        if (!__all_sync(0xffffffffu, mbar_wait_long(&raw[s], (rawph >> s) & 1u, ctl))) break;
         rawph ^= 1u << s;
         zero_tile_rows(slot_s(s), DVH / 64, BK, w.klen - (w.nkt - 1) * BK, BK, lane);
         fence_proxy_async_smem();

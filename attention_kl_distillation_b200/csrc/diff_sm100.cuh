@@ -82,6 +82,23 @@ __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int chunks, int ro
   }
 }
 
+// Waits for something that may come any time until the kernel's end (a ragged
+// tile some units ahead): ends with the phase, with an abort that another role
+// raised when one of its own bounded waits ran out, or after 1024 wait limits.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_try_wait(a, parity)) return true;
+    if (*c.abort) return false;
+    if (globaltimer_ns() - t0 > 1024 * c.limit_ns) {
+      raise_abort(c, kStatusTimeout);
+      return false;
+    }
+    __nanosleep(200);
+  }
+}
+
 // Transposes NP 16-byte pieces among each NP neighbouring lanes: lane i of such
 // a group starts with pieces 0..NP-1 of its own row and ends with piece i of the
 // group's rows 0..NP-1, so that one store of the group covers a row's NP pieces.

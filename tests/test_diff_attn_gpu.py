@@ -299,3 +299,73 @@ def test_captured_step_and_two_streams():
         assert torch.equal(a, b)
 
 
+
+
+def test_two_streams_at_once():
+    """Calls on two streams at the same time do not touch each other."""
+    import attention_kl_distillation_b200 as skl
+    sets = [make(1, 8, 4, 700, 700, 64, 128, seed=41 + k) for k in range(2)]
+
+    def step(ops, dO):
+        saved = skl.diff_attn_fwd(*ops, causal=True)
+        return (saved[0], *skl.diff_attn_bwd(dO, *ops, *saved, causal=True))
+
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(5):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[k].append(step(*sets[k]))
+    torch.cuda.synchronize()
+    assert skl.query_device_status() == 0
+    for w, runs in zip(want, got):
+        for r in runs:
+            assert all(torch.equal(a, b) for a, b in zip(w, r))
+
+
+def test_captured_autograd_step():
+    """A training step through autograd, captured with no eager graph of the leaves alive."""
+    import attention_kl_distillation_b200 as skl
+    ops, dO = make(1, 4, 2, 130, 130, 64, 64, seed=51)
+    leaves = [t.requires_grad_() for t in ops]
+
+    def step():
+        O = skl.diff_attn(*leaves, causal=True)
+        return (O.detach(), *torch.autograd.grad(O, leaves, dO))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = [t.clone() for t in step()]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for t in out:
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d,dv", [(64, 128), (128, 256)])
+def test_a_query_tile_per_multiprocessor(d, dv):
+    """Long sequences run one key head at a time: the first and last rows of every head against rows of a
+    smaller problem (the last 100 rows see the same keys under the bottom-right causal mask)."""
+    import attention_kl_distillation_b200 as skl
+    N, H = 148 * 128 + 77, 4
+    ops, dO = make(2, H, 2, N, N, d, dv, seed=61)
+    saved = skl.diff_attn_fwd(*ops, causal=True)
+    dQ1, _, dQ2 = skl.diff_attn_bwd(dO, *ops, *saved, causal=True, need=(True, False, True, False, False, False))[:3]
+    assert skl.query_device_status() == 0
+    Q1, K1, Q2, K2, V, lam = ops
+    for rows, keys in ((slice(0, 100), slice(0, 100)), (slice(N - 100, N), slice(0, N))):
+        r = Reference(Q1[:, :, rows], K1[:, :, keys], Q2[:, :, rows], K2[:, :, keys], V[:, :, keys], lam, True)
+        within("O", saved[0][:, :, rows], r.O, r.tol_O)
+        g = r.backward(dO[:, :, rows])
+        within("dQ1", dQ1[:, :, rows], *g["dQ1"])
+        within("dQ2", dQ2[:, :, rows], *g["dQ2"])

@@ -313,3 +313,55 @@ def test_write_past_the_cache_is_reported():
     assert torch.equal(cache, want)
     skl.paged_write((rows[:0],), (cache,), torch.zeros(0, dtype=torch.int64, device="cuda"))
     assert torch.equal(cache, want)
+
+
+def test_prompts_then_tokens():
+    """Served as it is used: a padded batch of prompts through diff_attn, their rows into the pages, then single
+    tokens through paged_write and diff_attn_paged; every output against the whole sequence in 64 bits."""
+    import attention_kl_distillation_b200 as skl
+    B, H, HK, d, dv, page, N, more = 3, 8, 2, 64, 128, 32, 90, 5
+    g = torch.Generator().manual_seed(77)
+    n = torch.tensor([90, 31, 64], dtype=torch.int32, device="cuda")
+    total = N + more
+    rnd = lambda h, w: torch.randn(B, total, h, w, generator=g).to(BF).cuda()  # noqa: E731
+    q1, k1, q2, k2, v = rnd(H, d), rnd(HK, d), rnd(H, d), rnd(HK, d), rnd(HK, dv)
+    lam = torch.rand(H, generator=g).to(BF).cuda()
+    caches = [torch.zeros(16, page, HK, w, dtype=BF, device="cuda") for w in (d, d, dv)]
+    table = torch.randperm(16, generator=g)[:B * 3].int().view(B, 3).cuda()
+    heads_first = [t.transpose(1, 2) for t in (q1, k1, q2, k2, v)]
+    O = skl.diff_attn(*(t[:, :, :N] for t in heads_first), lam, causal=True, q_lens=n, k_lens=n)
+    r = Reference(*(t[:, :, :N] for t in heads_first), lam, True, q_lens=n, k_lens=n)
+    within("prompt", O, r.O, r.tol_O)
+    at = torch.arange(N, device="cuda").expand(B, N)
+    slots = table.long().gather(1, at // page) * page + at % page
+    slots = torch.where(at < n.view(B, 1), slots, -1)     # the padding is not written
+    skl.paged_write([t[:, :N].reshape(B * N, HK, -1) for t in (k1, k2, v)], caches, slots.reshape(-1))
+    b = torch.arange(B, device="cuda")
+    for _ in range(more):
+        pos = n.long()
+        new = table.long()[b, pos // page] * page + pos % page
+        skl.paged_write([t[b, pos] for t in (k1, k2, v)], caches, new)
+        n = n + 1
+        got = skl.diff_attn_paged(q1[b, pos], caches[0], q2[b, pos], caches[1], caches[2], lam, table, n)
+        for s in range(B):
+            p = int(pos[s])
+            one = Reference(*(t[s:s + 1, :, sl] for t, sl in zip(heads_first, (slice(p, p + 1), slice(0, p + 1)) * 2
+                                                                 + (slice(0, p + 1),))), lam, True, factors=2)
+            within(f"token {p} of sequence {s}", got[s], one.O[0, :, 0], one.tol_O[0, :, 0])
+    assert skl.query_device_status() == 0
+
+
+def test_paged_calls_on_two_streams_at_once():
+    import attention_kl_distillation_b200 as skl
+    sets = [make([900, 3, 2000], 16, 4, 64, 128, seed=k) for k in range(2)]
+    want = [run(c, 2) for c in sets]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], [[], []]
+    for _ in range(10):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[k].append(run(sets[k], 2))
+    torch.cuda.synchronize()
+    assert skl.query_device_status() == 0
+    for w, runs in zip(want, got):
+        assert all(torch.equal(w, r) for r in runs)
