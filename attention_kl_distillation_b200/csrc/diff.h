@@ -123,13 +123,15 @@ struct DiffBwdParams {
   Strides so1, so2, so3;
   float c1, c2;  // s_t * log2(e)
   float s1, s2;
-  int nhalf;     // dV-only pass: value columns in groups of 128
+  int nhalf;     // dV-only pass: value columns in groups of 128; SEL 1: maps
+  int map0;      // SEL 1: the first map (0 or 1)
+  int after_pass;  // launched behind another pass, which it need not wait for
   int* status;
   unsigned long long wait_limit_ns;
 };
 enum DiffPass : int { kDiffKV = 0, kDiffQ = 1 };
-// sel: 1 map 1's dS, 2 map 2's dS, 4 dV.  diff_bwd_passes gives the launches a
-// head shape needs.
+// sel: 7 both maps and dV (d = 64), 3 both maps, 1 one map per unit (dv = 256),
+// 4 dV alone (d = 128).
 cudaError_t launch_diff_bwd(const DiffBwdParams& p, DiffPass pass, int d, int dv, int sel, bool f16,
                             int num_sms, cudaStream_t stream);
 

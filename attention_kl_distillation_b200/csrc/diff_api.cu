@@ -274,11 +274,14 @@ streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const strea
     SKL_TRY(map_of(*dO, pr.B, pr.H, pr.NQ, pr.dv, rq, pr.dtype, kv ? &p.tmC3 : &p.tmR3));
     return STREAMKL_OK;
   };
-  auto run = [&](skl::DiffPass pass, int sel, int nhalf) -> streamkl_status {
+  p.after_pass = 0;
+  auto run = [&](skl::DiffPass pass, int sel, int nhalf, int map0 = 0) -> streamkl_status {
     p.nhalf = nhalf;
+    p.map0 = map0;
     if (skl::launch_diff_bwd(p, pass, pr.d, pr.dv, sel, f16, sms, s) != cudaSuccess)
       return STREAMKL_ECUDA;
     skl::api_count_launches(1);
+    p.after_pass = 1;  // the passes share the records and nothing else
     return STREAMKL_OK;
   };
   auto put = [](const streamkl_tensor* t, void** out, skl::Strides* st) {
@@ -296,8 +299,7 @@ streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const strea
       if (pr.dv == 128) {
         if (dK1 || dK2) SKL_TRY(run(skl::kDiffKV, 3, 1));
       } else {
-        if (dK1) SKL_TRY(run(skl::kDiffKV, 1, 1));
-        if (dK2) SKL_TRY(run(skl::kDiffKV, 2, 1));
+        if (dK1 || dK2) SKL_TRY(run(skl::kDiffKV, 1, dK1 && dK2 ? 2 : 1, dK1 ? 0 : 1));
       }
       if (dV) SKL_TRY(run(skl::kDiffKV, 4, pr.dv / 128));
     }
@@ -310,8 +312,7 @@ streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const strea
     if (pr.dv <= 128) {
       SKL_TRY(run(skl::kDiffQ, 3, 1));
     } else {
-      if (dQ1) SKL_TRY(run(skl::kDiffQ, 1, 1));
-      if (dQ2) SKL_TRY(run(skl::kDiffQ, 2, 1));
+      SKL_TRY(run(skl::kDiffQ, 1, dQ1 && dQ2 ? 2 : 1, dQ1 ? 0 : 1));
     }
   }
   return STREAMKL_OK;

