@@ -92,17 +92,16 @@ struct DiffPrepParams {
   const float* LSE1;
   const float* LSE2;
   float* rec;  // [B*H][NQpad/64][kDiffRec][64]
-  float* sums; // [B*H][NQpad/64]: D2 summed over the rows of a step
   int NQpad, dv, f16;
 };
 cudaError_t launch_diff_prep(const DiffPrepParams& p, int num_sms, cudaStream_t stream);
 
-// dlam from the records' D2 (dlam of a row is -D2), summed over what lam is broadcast over.
+// dlam from the sums of P2 G that the kQ pass leaves (dlam of a row is minus the
+// row's), over what lam is broadcast over.
 struct DiffLamParams {
-  const float* rec;
-  const float* sums;
+  const float* d2;         // see DiffBwdParams
   void* out;               // contiguous [B or 1][H or 1][NQ or 1]
-  int B, H, NQ, NQpad;
+  int B, H, NQ;
   int eb, eh, en;          // extents of out
   int f32, f16;            // out's type: fp32, or fp16 / bf16
 };
@@ -125,6 +124,11 @@ struct DiffBwdParams {
   float s1, s2;
   int nhalf;     // dV-only pass: value columns in groups of 128; SEL 1: maps
   int map0;      // SEL 1: the first map (0 or 1)
+  // kQ, or null: sums over the keys of P2 G in fp32, a share per compute warpgroup.
+  // d2_rows: of every row, [4][B*H][rows padded to 128]; else of the rows of a warp
+  // together, [B*H][row tiles][4 warpgroups][4 warps].
+  float* d2;
+  int d2_rows;
   int after_pass;  // launched behind another pass, which it need not wait for
   int* status;
   unsigned long long wait_limit_ns;

@@ -103,6 +103,16 @@ int padded_rows(const streamkl_diff_problem& pr) {
   return (pr.NQ + skl::kDiffStep - 1) / skl::kDiffStep * skl::kDiffStep;
 }
 
+// Row records, then the shares of P2 G (four a row), in floats.
+struct DiffWorkspace {
+  size_t rec, d2;
+};
+DiffWorkspace diff_workspace(const streamkl_diff_problem& pr) {
+  const size_t BH = static_cast<size_t>(pr.B) * pr.H;
+  const size_t tiles = (static_cast<size_t>(pr.NQ) + skl::kDiffRows - 1) / skl::kDiffRows;
+  return {BH * padded_rows(pr) * skl::kDiffRec, BH * tiles * skl::kDiffRows * 4};
+}
+
 streamkl_status check_paged(const streamkl_paged_problem* pr) {
   if (!pr) return STREAMKL_EINVAL;
   if (pr->B < 1 || pr->H < 1 || pr->HK < 1 || pr->pages < 1 || pr->page_size < 1 ||
@@ -181,9 +191,8 @@ streamkl_status streamkl_diff_fwd(const streamkl_diff_problem* prob, const strea
 
 size_t streamkl_diff_bwd_workspace_size(const streamkl_diff_problem* prob) {
   if (check_diff(prob) != STREAMKL_OK) return 0;
-  // row records, then a sum for every 64 rows
-  const size_t rows = static_cast<size_t>(prob->B) * prob->H * static_cast<size_t>(padded_rows(*prob));
-  return round256((rows * skl::kDiffRec + rows / skl::kDiffStep) * sizeof(float));
+  const DiffWorkspace w = diff_workspace(*prob);
+  return round256((w.rec + w.d2) * sizeof(float));
 }
 
 streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const streamkl_tensor* dO,
@@ -229,30 +238,11 @@ streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const strea
   pp.LSE1 = LSE1;
   pp.LSE2 = LSE2;
   pp.rec = rec;
-  pp.sums = rec + static_cast<size_t>(pr.B) * pr.H * padded_rows(pr) * skl::kDiffRec;
   pp.NQpad = padded_rows(pr);
   pp.dv = pr.dv;
   pp.f16 = f16;
   if (skl::launch_diff_prep(pp, sms, s) != cudaSuccess) return STREAMKL_ECUDA;
   skl::api_count_launches(1);
-
-  if (dlam) {
-    skl::DiffLamParams lp;
-    lp.rec = rec;
-    lp.sums = pp.sums;
-    lp.out = dlam;
-    lp.B = pr.B;
-    lp.H = pr.H;
-    lp.NQ = pr.NQ;
-    lp.NQpad = pp.NQpad;
-    lp.eb = lam->b ? pr.B : 1;
-    lp.eh = lam->h ? pr.H : 1;
-    lp.en = lam->n ? pr.NQ : 1;
-    lp.f32 = pr.lam_fp32;
-    lp.f16 = f16;
-    if (skl::launch_diff_lam(lp, s) != cudaSuccess) return STREAMKL_ECUDA;
-    skl::api_count_launches(1);
-  }
 
   skl::DiffBwdParams p;
   p.s = shape;
@@ -275,6 +265,8 @@ streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const strea
     return STREAMKL_OK;
   };
   p.after_pass = 0;
+  p.d2 = nullptr;
+  p.d2_rows = lam->n != 0 || pr.NQ == 1;
   auto run = [&](skl::DiffPass pass, int sel, int nhalf, int map0 = 0) -> streamkl_status {
     p.nhalf = nhalf;
     p.map0 = map0;
@@ -304,16 +296,33 @@ streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const strea
       if (dV) SKL_TRY(run(skl::kDiffKV, 4, pr.dv / 128));
     }
   }
-  if (dQ1 || dQ2) {
+  if (dQ1 || dQ2 || dlam) {
     SKL_TRY(maps(false));
     put(dQ1, &p.out1, &p.so1);
     put(dQ2, &p.out2, &p.so2);
     put(nullptr, &p.out3, &p.so3);
+    if (dlam) p.d2 = rec + diff_workspace(pr).rec;
+    const bool map1 = dQ1, map2 = dQ2 || dlam;
     if (pr.dv <= 128) {
       SKL_TRY(run(skl::kDiffQ, 3, 1));
     } else {
-      SKL_TRY(run(skl::kDiffQ, 1, dQ1 && dQ2 ? 2 : 1, dQ1 ? 0 : 1));
+      SKL_TRY(run(skl::kDiffQ, 1, map1 && map2 ? 2 : 1, map1 ? 0 : 1));
     }
+  }
+  if (dlam) {
+    skl::DiffLamParams lp;
+    lp.d2 = p.d2;
+    lp.out = dlam;
+    lp.B = pr.B;
+    lp.H = pr.H;
+    lp.NQ = pr.NQ;
+    lp.eb = lam->b ? pr.B : 1;
+    lp.eh = lam->h ? pr.H : 1;
+    lp.en = lam->n ? pr.NQ : 1;
+    lp.f32 = pr.lam_fp32;
+    lp.f16 = f16;
+    if (skl::launch_diff_lam(lp, s) != cudaSuccess) return STREAMKL_ECUDA;
+    skl::api_count_launches(1);
   }
   return STREAMKL_OK;
 }

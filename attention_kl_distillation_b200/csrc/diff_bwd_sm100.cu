@@ -6,7 +6,9 @@
 //   A   = P1 - lam P2              dV   = A^T dO
 //   X1  = P1 (G - D1)              dQ1  = s1 X1 K1    dK1 = s1 X1^T Q1
 //   X2  = lam P2 (D2 - G)          dQ2  = s2 X2 K2    dK2 = s2 X2^T Q2
-//   dlam[i] = -D2[i], summed over what lam is broadcast over
+//   dlam[i] = -sum_j P2 G, summed over what lam is broadcast over (D2 again, but from
+//             the unrounded P2: as a sum of few large terms it would show the
+//             rounding of O2)
 //
 // Two passes of one kernel template, each with a resident 128-row tile R and
 // streamed 64-row tiles C, so that every gradient is accumulated in TMEM by one
@@ -168,13 +170,13 @@ template <class Lay, bool MASK, bool F16>
 __device__ __forceinline__ void form_p(uint32_t (&s1)[CPW], uint32_t (&s2)[CPW], const float* rr,
                                        const float (&rec)[kDiffRec], float c1, float c2, int lo,
                                        int hi, int map) {
-  // P1 over s1 and lam P2 over s2; one map alone: P1, or -lam P2, over s1
+  // P1 over s1 and P2 over s2; resident keys: lam P2, and one map alone P1 or -lam P2
   const float2 C1 = make_float2(c1, c1), C2 = make_float2(c2, c2);
 #pragma unroll
   for (int q = 0; q < CPW; q += 4) {
     float4 b1 = make_float4(rec[0], rec[0], rec[0], rec[0]);
     float4 b2 = make_float4(rec[1], rec[1], rec[1], rec[1]);
-    float4 lm = make_float4(rec[4], rec[4], rec[4], rec[4]);
+    float4 lm = make_float4(0.f, 0.f, 0.f, 0.f);
     if (Lay::KV) {
       if (Lay::S1) b1 = ld_shared_f4(rr + map * CB + q);
       if (Lay::S2) b2 = ld_shared_f4(rr + 1 * CB + q);
@@ -189,17 +191,16 @@ __device__ __forceinline__ void form_p(uint32_t (&s1)[CPW], uint32_t (&s2)[CPW],
         const float2 u = __ffma2_rn(x, C1, e ? make_float2(b1.z, b1.w) : make_float2(b1.x, b1.y));
         s1[i] = vx ? __float_as_uint(ex2(u.x)) : 0u;
         s1[i + 1] = vy ? __float_as_uint(ex2(u.y)) : 0u;
-        if (Lay::ONE && map) {
-          const float2 f = Lay::KV ? (e ? make_float2(lm.z, lm.w) : make_float2(lm.x, lm.y)) : make_float2(rec[4], rec[4]);
-          s1[i] = __float_as_uint(-__uint_as_float(s1[i]) * f.x);
-          s1[i + 1] = __float_as_uint(-__uint_as_float(s1[i + 1]) * f.y);
+        if (Lay::KV && Lay::ONE && map) {
+          s1[i] = __float_as_uint(-__uint_as_float(s1[i]) * (e ? lm.z : lm.x));
+          s1[i + 1] = __float_as_uint(-__uint_as_float(s1[i + 1]) * (e ? lm.w : lm.y));
         }
       }
       if (Lay::S2) {
         const float2 x = make_float2(__uint_as_float(s2[i]), __uint_as_float(s2[i + 1]));
         const float2 u = __ffma2_rn(x, C2, e ? make_float2(b2.z, b2.w) : make_float2(b2.x, b2.y));
-        const float2 r = __fmul2_rn(make_float2(vx ? ex2(u.x) : 0.f, vy ? ex2(u.y) : 0.f),
-                                    e ? make_float2(lm.z, lm.w) : make_float2(lm.x, lm.y));
+        float2 r = make_float2(vx ? ex2(u.x) : 0.f, vy ? ex2(u.y) : 0.f);
+        if (Lay::KV) r = __fmul2_rn(r, e ? make_float2(lm.z, lm.w) : make_float2(lm.x, lm.y));
         s2[i] = __float_as_uint(r.x);
         s2[i + 1] = __float_as_uint(r.y);
       }
@@ -324,6 +325,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           rec[2] = rec[3];
         }
       }
+      // kQ: X_t = P_t (f_t G + fd_t), f_1 = 1 and f_2 = -lam, fd_t = -f_t D_t
+      const float f1 = Lay::ONE && map ? -rec[4] : 1.f, fd1 = -f1 * rec[2];
+      const float f2 = -rec[4], fd2 = -f2 * rec[3];
+      float2 d2sum = make_float2(0.f, 0.f);
       const int steps = w.heads * w.tiles;
       int tile = 0;
       for (int t = 0; t < steps; ++t) {
@@ -398,13 +403,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const int i = q + 2 * e;
             if (Lay::X1) {
               const float2 d = e ? make_float2(d1.z, d1.w) : make_float2(d1.x, d1.y);
-              const float2 x = __fmul2_rn(pair(a, i), __ffma2_rn(d, NEG, pair(g, i)));
+              const float2 y = KV ? __ffma2_rn(d, NEG, pair(g, i))
+                                  : __ffma2_rn(pair(g, i), make_float2(f1, f1), make_float2(fd1, fd1));
+              const float2 x = __fmul2_rn(pair(a, i), y);
               w1[i / 2] = pack2<F16>(x.x, x.y);
+              if (!KV && Lay::ONE) d2sum = __ffma2_rn(pair(a, i), pair(g, i), d2sum);
             }
             if (Lay::X2) {
               const float2 d = e ? make_float2(d2.z, d2.w) : make_float2(d2.x, d2.y);
-              const float2 x = __fmul2_rn(pair(b, i), __ffma2_rn(pair(g, i), NEG, d));
+              const float2 y = KV ? __ffma2_rn(pair(g, i), NEG, d)
+                                  : __ffma2_rn(pair(g, i), make_float2(f2, f2), make_float2(fd2, fd2));
+              const float2 x = __fmul2_rn(pair(b, i), y);
               w2[i / 2] = pack2<F16>(x.x, x.y);
+              if (!KV) d2sum = __ffma2_rn(pair(b, i), pair(g, i), d2sum);
             }
           }
         }
@@ -441,6 +452,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // rows behind their sequence, and rows that see nothing, get exact zeros
       const bool live = steps > 0 && row < (KV ? e.l.k : e.l.q) &&
                         (KV || !p.s.causal || row + e.l.k - e.l.q >= 0);
+      if (!KV && p.d2 && (!Lay::ONE || p.map0 + e.half == 1)) {
+        float v = live ? d2sum.x + d2sum.y : 0.f;
+        const int nrt = (p.s.NQ + R - 1) / R, rt = e.r0 / R;
+        const size_t bh = static_cast<size_t>(e.b) * p.s.H + e.h;
+        if (p.d2_rows) {
+          p.d2[(static_cast<size_t>(ep) * p.s.B * p.s.H + bh) * (nrt * static_cast<size_t>(R)) + row] = v;
+        } else {
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+          if (lane == 0) p.d2[(bh * nrt + rt) * 16 + ep * 4 + quarter] = v;
+        }
+      }
       const int h = KV ? e.hk : e.h;
       // one output after the other, 16 columns at a time: a loop, so that its
       // values do not take registers from the steps
@@ -855,12 +878,6 @@ __global__ void __launch_bounds__(256) streamkl_diff_prep_kernel(const DiffPrepP
     __syncthreads();
     float* dst = p.rec + static_cast<long long>(u) * (CB * kDiffRec);
     for (int k = threadIdx.x; k < CB * kDiffRec; k += 256) dst[k] = out[k / CB][k % CB];
-    if (threadIdx.x < 32) {
-      float t = out[3][threadIdx.x] + out[3][threadIdx.x + 32];
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
-      if (threadIdx.x == 0) p.sums[u] = t;
-    }
     __syncthreads();
   }
 }
@@ -872,24 +889,18 @@ __device__ __forceinline__ void store_lam(const P& p, long long e, float v) {
   else static_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16_rn(v);
 }
 
-// One block per element of dlam: -sum of D2 over the rows it is broadcast over,
-// each thread a strided share in order, then a tree: the same sum every time.
-// Where the rows of a sequence are all summed (en = 1), the 64-row sums of the
-// preparation are read in place of the rows.
+// One block per element of dlam that sums whole rows' axes (en = 1): each thread a
+// strided share in order, then a tree: the same sum every time.
 __global__ void __launch_bounds__(256) streamkl_diff_lam_kernel(const DiffLamParams p) {
   __shared__ float part[8];
   const int e = blockIdx.x;
-  const int n0 = e % p.en, h0 = e / p.en % p.eh, b0 = e / p.en / p.eh;
+  const int h0 = e % p.eh, b0 = e / p.eh;
   const int nb = p.eb == 1 ? p.B : 1, nh = p.eh == 1 ? p.H : 1;
-  const int steps = p.NQpad / CB;
+  const int n = (p.NQ + R - 1) / R * 16;
   float s = 0.f;
   for (int q = 0; q < nb * nh; ++q) {
-    const long long bh = static_cast<long long>(b0 + q / nh) * p.H + h0 + q % nh;
-    if (p.en == 1) {
-      for (int k = threadIdx.x; k < steps; k += blockDim.x) s += p.sums[bh * steps + k];
-    } else if (threadIdx.x == q % blockDim.x) {
-      s += p.rec[(bh * p.NQpad + (n0 / CB) * CB) * kDiffRec + 3 * CB + n0 % CB];
-    }
+    const float* d = p.d2 + (static_cast<size_t>(b0 + q / nh) * p.H + h0 + q % nh) * n;
+    for (int k = threadIdx.x; k < n; k += blockDim.x) s += d[k];
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
@@ -902,14 +913,21 @@ __global__ void __launch_bounds__(256) streamkl_diff_lam_kernel(const DiffLamPar
   }
 }
 
-// dlam of every row by itself (lam has an element per row): one thread a row.
+// dlam with an element per row (en = NQ), one thread each.
 __global__ void __launch_bounds__(256) streamkl_diff_lam_rows_kernel(const DiffLamParams p) {
-  const long long total = static_cast<long long>(p.B) * p.H * p.NQ;
+  const long long total = static_cast<long long>(p.eb) * p.eh * p.NQ;
+  const size_t pad = static_cast<size_t>((p.NQ + R - 1) / R) * R, BH = static_cast<size_t>(p.B) * p.H;
+  const int nb = p.eb == 1 ? p.B : 1, nh = p.eh == 1 ? p.H : 1;
   for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < total;
        e += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const int i = static_cast<int>(e % p.NQ);
-    const long long bh = e / p.NQ;
-    store_lam(p, e, -p.rec[(bh * p.NQpad + (i / CB) * CB) * kDiffRec + 3 * CB + i % CB]);
+    const int i = static_cast<int>(e % p.NQ), h0 = static_cast<int>(e / p.NQ % p.eh),
+              b0 = static_cast<int>(e / p.NQ / p.eh);
+    float s = 0.f;
+    for (int q = 0; q < nb * nh; ++q) {
+      const float* d = p.d2 + (static_cast<size_t>(b0 + q / nh) * p.H + h0 + q % nh) * pad + i;
+      s += (d[0] + d[BH * pad]) + (d[2 * BH * pad] + d[3 * BH * pad]);
+    }
+    store_lam(p, e, -s);
   }
 }
 
@@ -937,7 +955,7 @@ cudaError_t launch_diff_prep(const DiffPrepParams& p, int num_sms, cudaStream_t 
 
 cudaError_t launch_diff_lam(const DiffLamParams& p, cudaStream_t stream) {
   const long long n = static_cast<long long>(p.eb) * p.eh * p.en;
-  if (p.eb == p.B && p.eh == p.H && p.en == p.NQ) {
+  if (p.en > 1 || p.NQ == 1) {
     const long long blocks = (n + 255) / 256;
     streamkl_diff_lam_rows_kernel<<<static_cast<int>(blocks < 2048 ? blocks : 2048), 256, 0, stream>>>(p);
   } else {

@@ -324,7 +324,7 @@ streamkl_status streamkl_diff_fwd(const streamkl_diff_problem *prob, const strea
                                   const streamkl_tensor *O2, float *LSE1, float *LSE2,
                                   streamkl_stream_t stream);
 
-/* Workspace bytes of streamkl_diff_bwd: five fp32 per query row and one per 64.  0 on a bad problem. */
+/* Workspace bytes of streamkl_diff_bwd: nine fp32 per query row.  0 on a bad problem. */
 size_t streamkl_diff_bwd_workspace_size(const streamkl_diff_problem *prob);
 
 /*

@@ -9,6 +9,7 @@ Bounds (per element, worst case; u = half a step of the inputs' 16-bit type, rel
   D_t   sum |dO| (error of O_t, which is read back in 16 bits)
   X1    P1 (G - D1): u + c of the value, P1 times the errors of G and D1;  X2 alike
   dQ, dK, dV  the error of the 16-bit factor times the other factor's size, u of the result
+  dlam  c of each P2 G and the error of G, in fp32 throughout; u of the result
 A rounded factor is also off by half fp16's smallest step (2^-25) or, in bf16, by what is flushed to
 zero (2^-126), and so is P: the hardware exponential returns 0 for results under 2^-126, an absolute
 error of that much, whatever the factors G - D or V beside it. Every fp32 sum of n terms adds n 2^-23
@@ -126,7 +127,10 @@ class Reference:
         out["dV"] = (group_sum(v, self.HK), group_sum(e, self.HK))
         for n, (v, e) in out.items():
             out[n] = (v, e * (1 + u) + u * v.abs() + t)
-        dl, el = -D[1].squeeze(-1), eD2.squeeze(-1) + 2.0 ** -20 * D[1].abs().squeeze(-1)
+        # sums over the keys of the unrounded P2 G; 512: terms one after another of the sums over rows
+        size = (self.P[1] * G.abs()).sum(-1)
+        dl = -D[1].squeeze(-1)
+        el = (self.P[1] * (c * G.abs() + eG)).sum(-1) + (self.NK + 512) * eps * size + FLUSH * G.abs().sum(-1)
         shape = (1, self.lam_shape[0], 1) if len(self.lam_shape) == 1 else self.lam_shape or (1, 1, 1)
         axes = [k for k, n in enumerate(shape) if n == 1 and dl.shape[k] != 1]
         if axes:

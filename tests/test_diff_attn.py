@@ -172,8 +172,8 @@ def test_backward_abi_refuses():
                 dict(ws=None), dict(ws=B._vp(64)), dict(n=ctypes.c_size_t(64))):
         assert raw_bwd(problem(), **bad) == B.EINVAL, bad
     assert raw_bwd(problem(d=96)) == B.EUNSUPPORTED
-    for nq, rows in ((9, 64), (64, 64), (65, 128)):   # a record of 5 per row, a sum per 64 rows
-        need = 2 * 4 * (rows * 5 + rows // 64) * 4
+    for nq, rows in ((9, 64), (64, 64), (65, 128)):   # a record of 5 per row of 64, 4 sums per row of 128
+        need = 2 * 4 * (rows * 5 + 128 * 4) * 4
         assert 0 <= D.diff_attn_workspace_size(2, 4, 2, nq, 12, 64, 64) - need < 256
     assert D.diff_attn_workspace_size(2, 4, 3, 9, 12, 64, 64) == 0
 
