@@ -94,7 +94,7 @@ struct DiffPrepParams {
   float* rec;  // [B*H][NQpad/64][kDiffRec][64]
   int NQpad, dv, f16;
 };
-cudaError_t launch_diff_prep(const DiffPrepParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_diff_prep(const DiffPrepParams& p, cudaStream_t stream);
 
 // dlam from the sums of P2 G that the kQ pass leaves (dlam of a row is minus the
 // row's), over what lam is broadcast over.
@@ -169,8 +169,27 @@ size_t paged_workspace_bytes(int dv, int maps, int num_sms);
 cudaError_t launch_paged(const PagedParams& p, int d, int dv, bool f16, int num_sms,
                          cudaStream_t stream);
 
+// Division of numbers below 2^31 by a divisor known on the host: with
+// s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1, n / d is
+// (mulhi(n, m) + n) >> s (division by invariant integers using multiplication,
+// Granlund and Montgomery 1994).
+struct FastDiv {
+  unsigned m = 0;
+  int s = 0;
+  FastDiv() = default;
+  explicit FastDiv(unsigned d) {
+    while ((1ull << s) < d) ++s;
+    m = static_cast<unsigned>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ unsigned operator()(unsigned n) const { return (__umulhi(n, m) + n) >> s; }
+#endif
+};
+
 constexpr int kPagedWriteMax = 4;
 struct PagedWriteParams {
+  FastDiv by_vecs[kPagedWriteMax], by_token[kPagedWriteMax];  // pieces of a head's row, of a token
+  FastDiv by_page;                                            // rows of a page
   const void* rows[kPagedWriteMax];
   void* caches[kPagedWriteMax];
   long long row_t[kPagedWriteMax], row_h[kPagedWriteMax];   // strides of the rows [T][HK][width], bytes

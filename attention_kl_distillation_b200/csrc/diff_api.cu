@@ -241,7 +241,7 @@ streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const strea
   pp.NQpad = padded_rows(pr);
   pp.dv = pr.dv;
   pp.f16 = f16;
-  if (skl::launch_diff_prep(pp, sms, s) != cudaSuccess) return STREAMKL_ECUDA;
+  if (skl::launch_diff_prep(pp, s) != cudaSuccess) return STREAMKL_ECUDA;
   skl::api_count_launches(1);
 
   skl::DiffBwdParams p;
@@ -401,7 +401,7 @@ streamkl_status streamkl_paged_write(int n, const streamkl_tensor* rows,
                                      int page_size, streamkl_stream_t stream) {
   if (n < 1 || n > skl::kPagedWriteMax || !rows || !caches || !widths) return STREAMKL_EINVAL;
   if (T < 1 || HK < 1 || pages < 1 || page_size < 1 || (slots_int64 & ~1)) return STREAMKL_EINVAL;
-  if (static_cast<int64_t>(pages) * page_size > UINT32_MAX) return STREAMKL_EINVAL;
+  if (static_cast<int64_t>(pages) * page_size > INT32_MAX) return STREAMKL_EINVAL;
   if (!slots || !aligned(slots, slots_int64 ? 8 : 4)) return STREAMKL_EINVAL;
   skl::PagedWriteParams p;
   for (int k = 0; k < n; ++k) {
@@ -417,9 +417,12 @@ streamkl_status streamkl_paged_write(int n, const streamkl_tensor* rows,
     p.slot[k] = caches[k].n * 2;
     p.head[k] = caches[k].h * 2;
     p.vecs[k] = widths[k] / 8;
+    p.by_vecs[k] = skl::FastDiv(static_cast<unsigned>(p.vecs[k]));
+    p.by_token[k] = skl::FastDiv(static_cast<unsigned>(HK * p.vecs[k]));
   }
   p.slots = slots;
   p.slots64 = slots_int64;
+  p.by_page = skl::FastDiv(static_cast<unsigned>(page_size));
   p.n = n;
   p.T = T;
   p.HK = HK;

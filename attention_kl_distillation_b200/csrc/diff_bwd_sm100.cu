@@ -816,69 +816,63 @@ cudaError_t launch_type(const DiffBwdParams& p, DiffPass pass, int d, int dv, in
 }
 
 // Row records: D2 = <dO, O2>, D1 = <dO, O> + lam D2 (O = O1 - lam O2).  A block
-// takes 64 rows, DV / 8 lanes a row, so that every thread has its share of
-// dO, O and O2 (16 bytes of each, DV / 32 rows) in flight at once: bound by HBM.
+// takes 64 rows, DV / 8 lanes a row; bound by HBM (or L2, behind the forward).
 template <int DV, bool F16>
-__global__ void __launch_bounds__(256) streamkl_diff_prep_kernel(const DiffPrepParams p) {
+__global__ void __launch_bounds__(256, 4) streamkl_diff_prep_kernel(const DiffPrepParams p) {
   constexpr int L = DV / 8, RPT = CB * L / 256;  // lanes a row, rows a thread
-  __shared__ float out[kDiffRec][CB];
-  const int steps = p.NQpad / CB, units = p.s.B * p.s.H * steps;
+  __shared__ float out[4][CB];  // [2] <dO, O>, [3] <dO, O2>
+  const int steps = p.NQpad / CB, u = blockIdx.x;
+  const int bh = u / steps, i0 = (u - bh * steps) * CB;
+  const int b = bh / p.s.H, h = bh - b * p.s.H;
+  const Lens l = diff_lens(p.s, b);
+  auto sees = [&](int i) { return i < l.q && l.k > 0 && (!p.s.causal || i + l.k - l.q >= 0); };
+  // what needs one thread a row is on its way first
+  float n1 = -INFINITY, n2 = -INFINITY, lam = 0.f;
+  if (threadIdx.x < CB && sees(i0 + threadIdx.x)) {
+    const long long v = static_cast<long long>(bh) * p.s.NQ + i0 + threadIdx.x;
+    n1 = -p.LSE1[v] * kLog2e;
+    n2 = -p.LSE2[v] * kLog2e;
+    lam = load_lam(p.lam, b, h, i0 + threadIdx.x, F16);
+  }
   const int sub = threadIdx.x % L, r0 = threadIdx.x / L;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int bh = u / steps, i0 = (u - bh * steps) * CB;
-    const int b = bh / p.s.H, h = bh - b * p.s.H;
-    const Lens l = diff_lens(p.s, b);
-    uint4 x[RPT], y[RPT], z[RPT];
-    bool seen[RPT];
 #pragma unroll
-    for (int k = 0; k < RPT; ++k) {
-      const int i = i0 + r0 + k * (256 / L);
-      seen[k] = i < l.q && l.k > 0 && (!p.s.causal || i + l.k - l.q >= 0);
-      x[k] = y[k] = z[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (seen[k]) {
-        const long long oo = b * p.so.b + h * p.so.h + i * p.so.n + sub * 8;
-        x[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dO) + b * p.sdo.b +
-                                               h * p.sdo.h + i * p.sdo.n + sub * 8);
-        y[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.O) + oo);
-        z[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.O2) + oo);
-      }
+  for (int k = 0; k < RPT; ++k) {
+    const int row = r0 + k * (256 / L), i = i0 + row;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x, z = x;
+    if (sees(i)) {
+      const long long oo = b * p.so.b + h * p.so.h + i * p.so.n + sub * 8;
+      x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dO) + b * p.sdo.b + h * p.sdo.h +
+                                          i * p.sdo.n + sub * 8);
+      y = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.O) + oo);
+      z = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.O2) + oo);
+    }
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w}, zs[4] = {z.x, z.y, z.z, z.w};
+    float d = 0.f, d2 = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = unpack2<F16>(xs[e]), o = unpack2<F16>(ys[e]), o2 = unpack2<F16>(zs[e]);
+      d = fmaf(a.x, o.x, fmaf(a.y, o.y, d));
+      d2 = fmaf(a.x, o2.x, fmaf(a.y, o2.y, d2));
     }
 #pragma unroll
-    for (int k = 0; k < RPT; ++k) {
-      const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, ys[4] = {y[k].x, y[k].y, y[k].z, y[k].w},
-                     zs[4] = {z[k].x, z[k].y, z[k].z, z[k].w};
-      float d = 0.f, d2 = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 a = unpack2<F16>(xs[e]), o = unpack2<F16>(ys[e]), o2 = unpack2<F16>(zs[e]);
-        d = fmaf(a.x, o.x, fmaf(a.y, o.y, d));
-        d2 = fmaf(a.x, o2.x, fmaf(a.y, o2.y, d2));
-      }
-#pragma unroll
-      for (int s = L / 2; s > 0; s >>= 1) {
-        d += __shfl_xor_sync(0xffffffffu, d, s);
-        d2 += __shfl_xor_sync(0xffffffffu, d2, s);
-      }
-      if (sub == 0) {
-        const int row = r0 + k * (256 / L), i = i0 + row;
-        float lam = 0.f, n1 = -INFINITY, n2 = -INFINITY;
-        if (seen[k]) {
-          const long long v = static_cast<long long>(bh) * p.s.NQ + i;
-          lam = load_lam(p.lam, b, h, i, F16);
-          n1 = -p.LSE1[v] * kLog2e;
-          n2 = -p.LSE2[v] * kLog2e;
-        }
-        out[0][row] = n1;
-        out[1][row] = n2;
-        out[2][row] = fmaf(lam, d2, d);
-        out[3][row] = d2;
-        out[4][row] = lam;
-      }
+    for (int s = L / 2; s > 0; s >>= 1) {
+      d += __shfl_xor_sync(0xffffffffu, d, s);
+      d2 += __shfl_xor_sync(0xffffffffu, d2, s);
     }
-    __syncthreads();
-    float* dst = p.rec + static_cast<long long>(u) * (CB * kDiffRec);
-    for (int k = threadIdx.x; k < CB * kDiffRec; k += 256) dst[k] = out[k / CB][k % CB];
-    __syncthreads();
+    if (sub == 0) {
+      out[2][row] = d;
+      out[3][row] = d2;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < CB) {
+    const int row = threadIdx.x;
+    float* dst = p.rec + static_cast<long long>(u) * (CB * kDiffRec) + row;
+    dst[0 * CB] = n1;
+    dst[1 * CB] = n2;
+    dst[2 * CB] = fmaf(lam, out[3][row], out[2][row]);
+    dst[3 * CB] = out[3][row];
+    dst[4 * CB] = lam;
   }
 }
 
@@ -939,9 +933,8 @@ cudaError_t launch_diff_bwd(const DiffBwdParams& p, DiffPass pass, int d, int dv
              : launch_type<false>(p, pass, d, dv, sel, num_sms, stream);
 }
 
-cudaError_t launch_diff_prep(const DiffPrepParams& p, int num_sms, cudaStream_t stream) {
-  const int units = p.s.B * p.s.H * (p.NQpad / CB);
-  const int grid = units < num_sms * 8 ? units : num_sms * 8;
+cudaError_t launch_diff_prep(const DiffPrepParams& p, cudaStream_t stream) {
+  const int grid = p.s.B * p.s.H * (p.NQpad / CB);
   auto run = [&](auto f16) {
     constexpr bool F16 = decltype(f16)::value;
     if (p.dv == 64) streamkl_diff_prep_kernel<64, F16><<<grid, 256, 0, stream>>>(p);

@@ -736,14 +736,17 @@ __global__ void __launch_bounds__(256) streamkl_paged_write_kernel(const __grid_
   constexpr int kBlock = 256 * STEPS;
   for (long long base = static_cast<long long>(blockIdx.x) * kBlock; base < total;
        base += static_cast<long long>(gridDim.x) * kBlock) {
-    const int t0 = static_cast<int>(base / per), r0 = static_cast<int>(base - static_cast<long long>(t0) * per);
+    // one wide division a block and step; the others by multiplication
+    const int t0 = static_cast<int>(base / per);
+    const unsigned r0 = static_cast<unsigned>(base - static_cast<long long>(t0) * per) + threadIdx.x;
     uint4 x[STEPS];
     uint8_t* dst[STEPS];
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
       dst[k] = nullptr;
-      const int i = r0 + k * 256 + static_cast<int>(threadIdx.x);  // piece, counted from token t0
-      const int dt = i / per, r = i - dt * per, h = r / vecs, v = r - h * vecs, t = t0 + dt;
+      const unsigned i = r0 + k * 256;  // piece, counted from token t0
+      const unsigned dt = p.by_token[w](i), r = i - dt * per, h = p.by_vecs[w](r), v = r - h * vecs;
+      const long long t = static_cast<long long>(t0) + dt;
       if (t >= p.T) continue;
       const long long slot = p.slots64 ? static_cast<const long long*>(p.slots)[t]
                                        : static_cast<const int*>(p.slots)[t];
@@ -752,8 +755,8 @@ __global__ void __launch_bounds__(256) streamkl_paged_write_kernel(const __grid_
         atomicCAS(p.status, 0, static_cast<int>(STREAMKL_EDEVICE));
         continue;
       }
-      // slots of the cache fit in 32 bits: pages * page_size does
-      const unsigned page = static_cast<unsigned>(slot) / static_cast<unsigned>(p.page_size);
+      // slots of the cache fit in 31 bits: pages * page_size does
+      const unsigned page = p.by_page(static_cast<unsigned>(slot));
       const unsigned row = static_cast<unsigned>(slot) - page * static_cast<unsigned>(p.page_size);
       x[k] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.rows[w]) +
                                              t * p.row_t[w] + h * p.row_h[w] + v * 16);

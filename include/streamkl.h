@@ -394,7 +394,7 @@ streamkl_status streamkl_paged_attn(const streamkl_paged_problem *prob, const st
  * slots[t] = page * page_size + row.  slots: int32, or int64 with slots_int64.
  * A negative slot is skipped; one past the cache is skipped and recorded
  * (STREAMKL_EDEVICE).  Slots are distinct: of two rows with one slot either may
- * stay, in pieces of 16 bytes.  Elements have 2 bytes; widths are multiples of 8.
+ * stay, in pieces of 16 bytes.  Elements have 2 bytes; widths are multiples of 8; pages * page_size < 2^31.
  * The rest of the caches is left as it was.
  */
 streamkl_status streamkl_paged_write(int n, const streamkl_tensor *rows,

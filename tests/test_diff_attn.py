@@ -205,7 +205,7 @@ def test_write_abi_refuses():
                                             wide, T, HK, pages, page, None)
 
     for bad in (dict(n=0), dict(n=5), dict(T=0), dict(HK=0), dict(pages=0), dict(page=0), dict(width=12), dict(width=0),
-                dict(slots=0), dict(slots=4), dict(wide=2), dict(pages=1 << 20, page=1 << 13), dict(row=(0, 0, 64, 128)), dict(row=(256, 0, 0, 128)),
+                dict(slots=0), dict(slots=4), dict(wide=2), dict(pages=1 << 20, page=1 << 11), dict(row=(0, 0, 64, 128)), dict(row=(256, 0, 0, 128)),
                 dict(cache=(520, 2048, 64, 128)), dict(cache=(512, 2044, 64, 128))):
         assert call(**bad) == B.EINVAL, bad
 
