@@ -117,7 +117,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // about half as many groups as CTAs.
 struct Deal {
   int g, blocks, hw, groups, tile;
-  __device__ __forceinline__ Deal(const PagedParams& p, int teams, int grid) {
+  __host__ __device__ __forceinline__ Deal(const PagedParams& p, int teams, int grid) {
     g = p.H / p.HK;
     blocks = (g + HB - 1) / HB;
     const int items = p.HK * blocks;
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int c = blockIdx.x + 1, mine = blockIdx.y;
   const int4 cut = p.cuts[c];  // sequence, group, parts
   const int parts = cut.z;
-  if (parts == 0 || mine >= deal.hw) return;
+  if (parts == 0) return;
   Cursor cur;
   cur.group = cut.y;
   cur.head(deal, mine);
@@ -704,7 +704,7 @@ cudaError_t launch_t(const PagedParams& p, int num_sms, cudaStream_t stream) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(num_sms - 1, Lay::TEAMS);
+  cfg.gridDim = dim3(num_sms - 1, Deal(p, Lay::TEAMS, num_sms).hw);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 2 * static_cast<size_t>(num_sms) * MAPS * HB * sizeof(float);
   cfg.stream = stream;

@@ -316,7 +316,8 @@ def diff_attn_fwd(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens
     [B, H, NQ] with extents of 1 broadcast, in the inputs' type or fp32.  ``q_lens`` / ``k_lens``
     (int32 [B]) give the valid rows of a right-padded batch; the causal mask is bottom-right
     aligned on them (key j is visible from row i when j <= i + k_len - q_len), so a padded
-    self-attention batch passes both.  Rows that see no key give O = 0 and LSE = -inf.
+    self-attention batch passes both.  Rows that see no key give O = 0 and LSE = -inf.  Scales of
+    None (or <= 0) are 1/sqrt(d).
     O2 = P2 V and the LSEs are what ``diff_attn_bwd`` needs; ``save=False`` leaves them out (None).
     ``out`` may hold a preallocated O, and with ``save`` O2, LSE1, LSE2."""
     lam = _lam(lam)
