@@ -21,8 +21,8 @@ __all__ = [*_BINDING_NAMES, *_DIFF_NAMES]
 
 
 def __getattr__(name):
-    if name in _BINDING_NAMES:
-        return getattr(importlib.import_module(".binding", __name__), name)
-    if name in _DIFF_NAMES:
-        return getattr(importlib.import_module(".diff", __name__), name)
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    module = ".binding" if name in _BINDING_NAMES else ".diff" if name in _DIFF_NAMES else None
+    if module is None:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    value = globals()[name] = getattr(importlib.import_module(module, __name__), name)
+    return value

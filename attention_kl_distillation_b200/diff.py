@@ -288,7 +288,9 @@ class _DiffPlan:
         self.rows, self.out, self.q = (B, H, NQ), (B, H, NQ, dv), Q1
         self.empty = 0 in self.out or HK == 0
         self.out_shape, self.out_back = _like_shape(Q1.shape, Q1.stride, dv)
+        self.grads = [_like_shape(m.shape, m.stride, m.shape[-1]) for m in (Q1, K1, Q2, K2, V)]
         self.fwd = {}   # the forward's C structs for outputs in Q1's memory order, with and without O2
+        self.bwd = {}   # the backward's, by the gradients asked for and the layouts of dO and the state
         self.no_keys = NK == 0
         self.prob = diff_problem(B, H, HK, NQ, NK, d, dv, causal, s1, s2, Q1.dtype, lam.dtype == torch.float32)
         self.prob_at = ctypes.addressof(self.prob)
@@ -322,6 +324,10 @@ def diff_attn_fwd(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens
     ``out`` may hold a preallocated O, and with ``save`` O2, LSE1, LSE2."""
     lam = _lam(lam)
     plan = _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2)
+    return _forward(plan, Q1, K1, Q2, K2, V, lam, q_lens, k_lens, save, out)
+
+
+def _forward(plan, Q1, K1, Q2, K2, V, lam, q_lens, k_lens, save, out):
     if out is None:
         O, O2 = (Q1.new_empty(plan.out_shape) if k == 0 or save else None for k in range(2))
         if plan.out_back is not None:
@@ -361,7 +367,6 @@ def diff_attn_workspace_size(B, H, HK, NQ, NK, d, dv, causal=False) -> int:
     return int(_lib.streamkl_diff_bwd_workspace_size(ctypes.addressof(prob)))
 
 
-@functools.lru_cache(maxsize=512)
 def _bwd_structs(plan, dO, O, O2, LSE1, LSE2, grads):
     for name, m in (("dO", dO), ("O", O), ("O2", O2)):
         _check(name, m, plan.out, plan.q, "[B, H, NQ, dv]")
@@ -383,9 +388,15 @@ def diff_attn_bwd(dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, causal=False, s
     16-bit operands allow, and fp16 training wants the usual loss scale.
     ``out`` may pass preallocated gradients (None entries are skipped), ``workspace`` a device buffer
     of at least ``diff_attn_workspace_size`` bytes, 256-byte aligned."""
-    shape_lam, lam = lam, _lam(lam)
+    lam = _lam(lam)
     plan = _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2)
+    return _backward(plan, dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens, tuple(need),
+                     workspace, out)
+
+
+def _backward(plan, dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens, need, workspace, out):
     inputs = (Q1, K1, Q2, K2, V)
+    key = structs = None
     if out is not None:
         if len(out) != 6:
             raise ValueError("out must hold six entries: dQ1, dK1, dQ2, dK2, dV, dlam (None skips one)")
@@ -400,12 +411,19 @@ def diff_attn_bwd(dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, causal=False, s
     else:
         if len(need) != 6:
             raise ValueError("need must hold six entries: dQ1, dK1, dQ2, dK2, dV, dlam")
-        outs = [_like(_meta(t), t.shape[-1]) if want else None for t, want in zip(inputs, need)]
-        outs.append(torch.empty(shape_lam.shape, dtype=lam.dtype, device=lam.device) if need[5] else None)
-    if all(o is None for o in outs):
+        key = (need, *_keys(dO, O, O2, LSE1, LSE2))
+        structs = plan.bwd.get(key)
+        outs = []
+        for (shape, back), want in zip(plan.grads, need):
+            o = Q1.new_empty(shape) if want else None
+            outs.append(o if o is None or back is None else o.permute(back))
+        outs.append(lam.new_empty(lam.shape) if need[5] else None)
+    if all([o is None for o in outs]):
         raise ValueError("no gradient is asked for")
-    structs = _bwd_structs(plan, _meta(dO), _meta(O), _meta(O2), _meta(LSE1), _meta(LSE2),
-                           tuple(map(_meta, outs[:5])))
+    if structs is None:
+        structs = _bwd_structs(plan, *map(_meta, (dO, O, O2, LSE1, LSE2)), tuple(map(_meta, outs[:5])))
+        if key is not None and len(plan.bwd) < 64:
+            plan.bwd[key] = structs
     if plan.empty or plan.no_keys:
         for o in outs:
             if o is not None:
@@ -421,22 +439,19 @@ def diff_attn_bwd(dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, causal=False, s
 
 class _DiffAttnFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, Q1, K1, Q2, K2, V, lam, causal, s1, s2, q_lens, k_lens):
-        O, O2, LSE1, LSE2 = diff_attn_fwd(Q1, K1, Q2, K2, V, lam, causal, s1, s2, q_lens, k_lens)
-        ctx.save_for_backward(Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens)
-        ctx.cfg = (causal, s1, s2)
-        return O
+    def forward(ctx, plan, Q1, K1, Q2, K2, V, lam, q_lens, k_lens):
+        saved = _forward(plan, Q1, K1, Q2, K2, V, lam, q_lens, k_lens, True, None)
+        ctx.save_for_backward(Q1, K1, Q2, K2, V, lam, *saved, q_lens, k_lens)
+        ctx.plan = plan
+        return saved[0]
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dO):
-        *state, q_lens, k_lens = ctx.saved_tensors
-        need = tuple(bool(x) for x in ctx.needs_input_grad[:6])
-        if not any(need):
-            return (None,) * 11
-        if dO.data_ptr() % 16 or not _layout_ok(_meta(dO)):  # an expanded or sliced upstream gradient
-            dO = dO.clone(memory_format=torch.contiguous_format)
-        return (*diff_attn_bwd(dO, *state, *ctx.cfg, q_lens, k_lens, need=need), *(None,) * 5)
+        need = ctx.needs_input_grad[1:7]
+        if dO.data_ptr() % 16 or not (dO.is_contiguous() or _layout_ok(_meta(dO))):
+            dO = dO.clone(memory_format=torch.contiguous_format)  # expanded or sliced
+        return (None, *_backward(ctx.plan, dO, *ctx.saved_tensors, need, None, None), None, None)
 
 
 def diff_attn(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens=None, k_lens=None):
@@ -444,9 +459,12 @@ def diff_attn(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens=Non
 
     Arguments as in ``diff_attn_fwd``.  O's axes are in Q1's memory order.  Where no gradient is
     wanted, nothing is saved."""
-    if torch.is_grad_enabled() and any([getattr(t, "requires_grad", False) for t in (Q1, K1, Q2, K2, V, lam)]):
-        return _DiffAttnFunction.apply(Q1, K1, Q2, K2, V, lam, causal, s1, s2, q_lens, k_lens)
-    return diff_attn_fwd(Q1, K1, Q2, K2, V, lam, causal, s1, s2, q_lens, k_lens, save=False)[0]
+    lam = _lam(lam)
+    plan = _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2)
+    if torch.is_grad_enabled() and (Q1.requires_grad or K1.requires_grad or Q2.requires_grad or
+                                    K2.requires_grad or V.requires_grad or lam.requires_grad):
+        return _DiffAttnFunction.apply(plan, Q1, K1, Q2, K2, V, lam, q_lens, k_lens)
+    return _forward(plan, Q1, K1, Q2, K2, V, lam, q_lens, k_lens, False, None)[0]
 
 
 class _PagedPlan:
