@@ -37,6 +37,23 @@ cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
   return e;
 }
 
+// Division of numbers below 2^31 by a divisor known on the host: with
+// s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1, n / d is
+// (mulhi(n, m) + n) >> s (division by invariant integers using multiplication,
+// Granlund and Montgomery 1994).
+struct FastDiv {
+  unsigned m = 0;
+  int s = 0;
+  FastDiv() = default;
+  explicit FastDiv(unsigned d) {
+    while ((1ull << s) < d) ++s;
+    m = static_cast<unsigned>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ unsigned operator()(unsigned n) const { return (__umulhi(n, m) + n) >> s; }
+#endif
+};
+
 // Element strides of a [B][H][N][d] tensor whose features are contiguous.
 struct Strides {
   long long b, h, n;
@@ -56,6 +73,7 @@ struct DiffShape {
   int B, H, HK, NQ, NK, causal;
   const int* q_lens;  // [B] or null: NQ
   const int* k_lens;  // [B] or null: NK
+  FastDiv by_H, by_HK, by_share;  // share = H / HK query heads per key head
 };
 
 constexpr int kDiffRows = 128;  // UMMA M: query rows (forward, dQ) or keys (dK, dV) per unit
@@ -72,8 +90,9 @@ struct DiffFwdParams {
   float* LSE1;  // [B][H][NQ] or null
   float* LSE2;
   float c1, c2;  // s_t * log2(e)
-  int nhalf;     // value columns in groups of 128 (dv = 256: 2)
-  int head_group;
+  int nhalf;     // value columns in groups of 128: 1, or 2 (dv = 256)
+  int head_group;  // heads visited together; divides B * H
+  FastDiv by_group, by_group_units;
   int* status;
   unsigned long long wait_limit_ns;
 };
@@ -122,7 +141,8 @@ struct DiffBwdParams {
   Strides so1, so2, so3;
   float c1, c2;  // s_t * log2(e)
   float s1, s2;
-  int nhalf;     // dV-only pass: value columns in groups of 128; SEL 1: maps
+  int nhalf;     // dV-only pass: value columns in groups of 128; SEL 1: maps; 1 or 2
+  FastDiv by_heads;  // B * HK (kKV) or B * H (kQ)
   int map0;      // SEL 1: the first map (0 or 1)
   // kQ, or null: sums over the keys of P2 G in fp32, a share per compute warpgroup.
   // d2_rows: of every row, [4][B*H][rows padded to 128]; else of the rows of a warp
@@ -168,23 +188,6 @@ size_t paged_cuts_bytes(int num_sms);
 size_t paged_workspace_bytes(int dv, int maps, int num_sms);
 cudaError_t launch_paged(const PagedParams& p, int d, int dv, bool f16, int num_sms,
                          cudaStream_t stream);
-
-// Division of numbers below 2^31 by a divisor known on the host: with
-// s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1, n / d is
-// (mulhi(n, m) + n) >> s (division by invariant integers using multiplication,
-// Granlund and Montgomery 1994).
-struct FastDiv {
-  unsigned m = 0;
-  int s = 0;
-  FastDiv() = default;
-  explicit FastDiv(unsigned d) {
-    while ((1ull << s) < d) ++s;
-    m = static_cast<unsigned>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
-  }
-#ifdef __CUDACC__
-  __device__ __forceinline__ unsigned operator()(unsigned n) const { return (__umulhi(n, m) + n) >> s; }
-#endif
-};
 
 constexpr int kPagedWriteMax = 4;
 struct PagedWriteParams {

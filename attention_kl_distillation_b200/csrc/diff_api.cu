@@ -74,7 +74,8 @@ streamkl_status map_of(const streamkl_tensor& t, int64_t B, int64_t heads, int64
 }
 
 skl::DiffShape shape_of(const streamkl_diff_problem& pr, const int* q_lens, const int* k_lens) {
-  return skl::DiffShape{pr.B, pr.H, pr.HK, pr.NQ, pr.NK, pr.causal, q_lens, k_lens};
+  return skl::DiffShape{pr.B, pr.H, pr.HK, pr.NQ, pr.NK, pr.causal, q_lens, k_lens,
+                        skl::FastDiv(pr.H), skl::FastDiv(pr.HK), skl::FastDiv(pr.H / pr.HK)};
 }
 
 skl::Lambda lambda_of(const streamkl_tensor& t, int fp32) {
@@ -181,6 +182,8 @@ streamkl_status streamkl_diff_fwd(const streamkl_diff_problem* prob, const strea
   // Smaller problems interleave all heads, which keeps the last wave short.
   const int nqt = (pr.NQ + skl::kDiffRows - 1) / skl::kDiffRows;
   p.head_group = nqt >= sms ? pr.H / pr.HK : pr.B * pr.H;
+  p.by_group = skl::FastDiv(p.head_group);
+  p.by_group_units = skl::FastDiv(static_cast<unsigned>(p.head_group) * nqt * p.nhalf);
   p.wait_limit_ns = skl::api_wait_limit_ns();
   if (skl::launch_diff_fwd(p, pr.d, pr.dv, pr.dtype == STREAMKL_FP16, sms,
                            reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
@@ -269,6 +272,7 @@ streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const strea
   p.d2_rows = lam->n != 0 || pr.NQ == 1;
   auto run = [&](skl::DiffPass pass, int sel, int nhalf, int map0 = 0) -> streamkl_status {
     p.nhalf = nhalf;
+    p.by_heads = skl::FastDiv(static_cast<unsigned>(pr.B) * (pass == skl::kDiffKV ? pr.HK : pr.H));
     p.map0 = map0;
     if (skl::launch_diff_bwd(p, pass, pr.d, pr.dv, sel, f16, sms, s) != cudaSuccess)
       return STREAMKL_ECUDA;

@@ -122,17 +122,16 @@ struct BwdUnit {
 template <int PASS>
 __device__ __forceinline__ BwdUnit decode(const DiffBwdParams& p, int u) {
   BwdUnit w;
-  const int off_first = 0;
-  w.half = u % p.nhalf;
-  u /= p.nhalf;
+  w.half = u & (p.nhalf - 1);
+  u >>= p.nhalf - 1;
+  const int tile = p.by_heads(u);
   if (PASS == kDiffKV) {
     // key tiles that the most rows see first, heads innermost
-    const int BH = p.s.B * p.s.HK;
-    const int bh = u % BH;
-    w.r0 = (u / BH) * R;
-    w.b = bh / p.s.HK;
-    w.hk = bh % p.s.HK;
-    w.heads = p.s.H / p.s.HK;
+    const int bh = u - tile * (p.s.B * p.s.HK);
+    w.r0 = tile * R;
+    w.b = p.s.by_HK(bh);
+    w.hk = bh - w.b * p.s.HK;
+    w.heads = p.s.by_HK(p.s.H);
     w.h = w.hk * w.heads;
     w.l = diff_lens(p.s, w.b);
     const int off = w.l.k - w.l.q;
@@ -143,13 +142,11 @@ __device__ __forceinline__ BwdUnit decode(const DiffBwdParams& p, int u) {
     w.c_first = first / CB;
     w.tiles = (w.r0 < w.l.k && first < w.hi) ? (w.hi + CB - 1) / CB - w.c_first : 0;
   } else {
-    const int BH = p.s.B * p.s.H;
-    const int nrt = (p.s.NQ + R - 1) / R;
-    const int bh = u % BH;
-    w.r0 = (nrt - 1 - u / BH) * R;
-    w.b = bh / p.s.H;
-    w.h = bh % p.s.H;
-    w.hk = w.h / (p.s.H / p.s.HK);
+    const int bh = u - tile * (p.s.B * p.s.H);
+    w.r0 = ((p.s.NQ + R - 1) / R - 1 - tile) * R;
+    w.b = p.s.by_H(bh);
+    w.h = bh - w.b * p.s.H;
+    w.hk = p.s.by_share(w.h);
     w.heads = 1;
     w.l = diff_lens(p.s, w.b);
     w.lo = 0;
@@ -157,7 +154,7 @@ __device__ __forceinline__ BwdUnit decode(const DiffBwdParams& p, int u) {
     int keys = w.l.k;
     if (p.s.causal) keys = min(keys, min(w.r0 + R, w.l.q) + w.l.k - w.l.q);
     if (w.r0 >= w.l.q) keys = 0;
-    w.c_first = off_first;
+    w.c_first = 0;
     w.tiles = keys > 0 ? (keys + CB - 1) / CB : 0;
   }
   return w;

@@ -70,20 +70,18 @@ struct FwdUnit {
 __device__ __forceinline__ FwdUnit decode(const DiffFwdParams& p, int u) {
   FwdUnit w;
   const int nqt = (p.s.NQ + R - 1) / R;
-  const int BH = p.s.B * p.s.H;
   // Heads in groups: within a group the query tiles that see the most keys
   // first, heads innermost, the value halves of a tile next to each other.
-  const int gs = min(p.head_group, BH);
-  const int g = u / (gs * nqt * p.nhalf);
-  const int gsize = min(gs, BH - g * gs);
+  const int gs = p.head_group;
+  const int g = p.by_group_units(u);
   int r = u - g * (gs * nqt * p.nhalf);
-  w.half = r % p.nhalf;
-  r /= p.nhalf;
-  const int bh = g * gs + r % gsize;
-  w.q0 = (nqt - 1 - r / gsize) * R;
-  w.b = bh / p.s.H;
-  w.h = bh % p.s.H;
-  w.hk = w.h / (p.s.H / p.s.HK);
+  w.half = r & (p.nhalf - 1);
+  r >>= p.nhalf - 1;
+  const int tile = p.by_group(r), bh = g * gs + r - tile * gs;
+  w.q0 = (nqt - 1 - tile) * R;
+  w.b = p.s.by_H(bh);
+  w.h = bh - w.b * p.s.H;
+  w.hk = p.s.by_share(w.h);
   const Lens l = diff_lens(p.s, w.b);
   w.qlen = l.q;
   w.klen = l.k;
