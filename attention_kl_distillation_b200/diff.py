@@ -170,6 +170,7 @@ def _lam(lam):
 
 
 def _scale(s):
+    """A scale's value when the call is made: plans are kept by it."""
     return float(s) if s is not None else 0.0
 
 
@@ -302,7 +303,7 @@ _diff_plan = _planned(_DiffPlan)
 
 
 def _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2):
-    return _diff_plan(*_keys(Q1, K1, Q2, K2, V, lam, q_lens, k_lens), bool(causal), s1, s2)
+    return _diff_plan(*_keys(Q1, K1, Q2, K2, V, lam, q_lens, k_lens), bool(causal), _scale(s1), _scale(s2))
 
 
 def _fwd_structs(plan, O, O2):
@@ -522,7 +523,7 @@ _paged_plan = _planned(_PagedPlan)
 
 def _paged(Q1, K1, Q2, K2, V, lam, table, lens, s1, s2, workspace, out):
     lam = _lam(lam)
-    plan = _paged_plan(*_keys(Q1, K1, Q2, K2, V, lam, table, lens, out), s1, s2)
+    plan = _paged_plan(*_keys(Q1, K1, Q2, K2, V, lam, table, lens, out), _scale(s1), _scale(s2))
     if out is None:
         out = Q1.new_empty(plan.out)
     if plan.empty or plan.no_keys:

@@ -113,6 +113,24 @@ def test_write_refuses():
             D.paged_write(r, c, s)
 
 
+def test_scales_are_read_at_every_call(monkeypatch):
+    """A scale passed as a tensor may change between calls: what is kept goes by its value."""
+    monkeypatch.setattr(D, "_check_cuda", lambda t: None)
+    o, s = ops(), torch.tensor(0.5)
+    plan = lambda: D._plan_of(*o.values(), None, None, False, s, s).prob  # noqa: E731
+    assert (plan().s1, plan().s2) == (0.5, 0.5)
+    s.fill_(0.25)
+    assert (plan().s1, plan().s2) == (0.25, 0.25)
+    c, kept = paged(), []
+    c.update(K1=c["K1"][:0], K2=c["K2"][:0], V=c["V"][:0])     # no pages: nothing is launched
+    planned = D._paged_plan
+    monkeypatch.setattr(D, "_paged_plan", lambda *k: kept.append(planned(*k)) or kept[-1])
+    D.diff_attn_paged(**c, s1=s, s2=s)
+    s.fill_(0.125)
+    D.diff_attn_paged(**c, s1=s, s2=s)
+    assert [(p.prob.s1, p.prob.s2) for p in kept] == [(0.25, 0.25), (0.125, 0.125)]
+
+
 # ---------------------------------------------------------------- C ABI
 def tensor(ptr, b=4096, h=1024, n=64):
     return ctypes.byref(D._Tensor(ptr, b, h, n))
