@@ -110,6 +110,8 @@ def _check(name, m, shape, like, what):
         raise ValueError(f"{name} must be bf16 or fp16, the same type as the other operands")
     if m.device != like.device:
         raise ValueError("tensors must be on one device")
+    if max(m.shape) >= 2 ** 31:
+        raise ValueError(f"{name} must have extents below 2^31")
     if 0 not in m.shape and not _layout_ok(m):
         raise ValueError(f"{name} must have contiguous features and outer strides that are positive "
                          "multiples of 8 elements")
@@ -488,7 +490,7 @@ class _PagedPlan:
         lam_strides = _lam_strides(lam, (B, H), Q1) if two else None
         if table is None or table.dtype != torch.int32 or len(table.shape) != 2 or table.shape[0] != B or \
                 table.device != Q1.device or (table.shape[1] > 1 and table.stride[1] != 1) or \
-                (B > 1 and table.stride[0] < table.shape[1]):
+                (B > 1 and table.stride[0] < table.shape[1]) or table.shape[1] >= 2 ** 31:
             raise ValueError("table must be an int32 tensor [B, pages of a sequence] on the inputs' device, "
                              "its rows contiguous and apart")
         if lens is None:

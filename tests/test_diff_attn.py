@@ -113,6 +113,21 @@ def test_write_refuses():
             D.paged_write(r, c, s)
 
 
+def test_extents_past_32_bits_are_refused():
+    """Sizes are passed as C ints, which would keep only their low bits."""
+    z = lambda *s: torch.empty(*s, dtype=BF, device="meta")  # noqa: E731
+    n = (1 << 32) + 8
+    o = dict(Q1=z(1, 2, 8, 64), K1=z(1, 2, n, 64), Q2=z(1, 2, 8, 64), K2=z(1, 2, n, 64), V=z(1, 2, n, 64), lam=z(2))
+    with pytest.raises(ValueError, match="2\\^31"):
+        D.diff_attn_fwd(**o)
+    with pytest.raises(ValueError, match="2\\^31"):
+        D.attn_paged(z(1, 2, 64), z(n, 16, 2, 64), z(n, 16, 2, 64), z(1, 4).int(), z(1).int())
+    with pytest.raises(ValueError, match="table"):
+        D.attn_paged(z(1, 2, 64), z(4, 16, 2, 64), z(4, 16, 2, 64), z(1, n).int(), z(1).int())
+    with pytest.raises(ValueError, match="2\\^31"):
+        D.paged_write((z(n, 2, 64),), (z(4, 16, 2, 64),), z(n).long())
+
+
 def test_scales_are_read_at_every_call(monkeypatch):
     """A scale passed as a tensor may change between calls: what is kept goes by its value."""
     monkeypatch.setattr(D, "_check_cuda", lambda t: None)
