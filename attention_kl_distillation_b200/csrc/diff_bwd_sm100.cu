@@ -107,11 +107,12 @@ struct BwdLay {
 };
 
 // A unit: 128 resident rows, and the streamed tiles [c_first, c_first + tiles)
-// of each of `heads` query heads (kQ: of one key head).
+// of each of `heads` query heads (kQ: of one key head).  `half`: the value half,
+// or with one map per unit (SEL 1) that map.
 struct BwdUnit {
   int b, h, hk, half, r0, c_first, tiles, heads, lo, hi;
   Lens l;
-  // SEL 1: the unit's map.  Streamed rows [lo, hi) are in the problem; a tile that reaches past either
+  // Streamed rows [lo, hi) are in the problem; a tile that reaches past either
   // end, yet not beyond the tensor, is ragged and cleaned before use.
   __device__ __forceinline__ bool ragged(int tile, int n) const {
     const int c0 = (c_first + tile) * CB;
