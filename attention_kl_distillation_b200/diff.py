@@ -287,6 +287,8 @@ class _DiffPlan:
         lam_strides = _lam_strides(lam, (B, H, NQ), Q1)
         _check_cuda(Q1.device)
         dv = V.shape[3]
+        self.keys = [Q1, K1, Q2, K2, V, lam, q_lens, k_lens]
+        self.options = causal, s1, s2
         self.device, self.dtype = Q1.device, Q1.dtype
         self.rows, self.out, self.q = (B, H, NQ), (B, H, NQ, dv), Q1
         self.empty = 0 in self.out or HK == 0
@@ -454,7 +456,14 @@ class _DiffAttnFunction(torch.autograd.Function):
         need = ctx.needs_input_grad[1:7]
         if dO.data_ptr() % 16 or not (dO.is_contiguous() or _layout_ok(_meta(dO))):
             dO = dO.clone(memory_format=torch.contiguous_format)  # expanded or sliced
-        return (None, *_backward(ctx.plan, dO, *ctx.saved_tensors, need, None, None), None, None)
+        Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens = ctx.saved_tensors
+        plan = ctx.plan
+        # hooks on saved tensors (offloading, say) may give them back in another layout
+        if _keys(Q1, K1, Q2, K2, V, lam, q_lens, k_lens) != plan.keys:
+            lam = _lam(lam)
+            plan = _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, *plan.options)
+        return (None, *_backward(plan, dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens, need,
+                                 None, None), None, None)
 
 
 def diff_attn(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens=None, k_lens=None):

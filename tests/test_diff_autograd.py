@@ -1,0 +1,70 @@
+"""CPU tests of how the differential and paged calls stand in autograd, with the launches replaced by a
+record of what the library would get."""
+import ctypes
+
+import pytest
+import torch
+
+from attention_kl_distillation_b200 import diff as D
+
+BF = torch.bfloat16
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library's calls as lists of arguments, structs of tensors as (pointer, strides)."""
+    made = []
+
+    def run(fn, where, device, *args):
+        made.append((where, [args[0], *(D._Tensor.from_address(a) if isinstance(a, int) and a in kept else a
+                                        for a in args[1:])]))
+
+    kept, at = set(), D._Structs.at
+
+    def structs(self, pointers):
+        block, addresses = at(self, pointers)
+        kept.update(a for a in addresses if a)
+        made.append(block)     # alive as long as the record
+        return block, addresses
+
+    monkeypatch.setattr(D, "_check_cuda", lambda device: None)
+    monkeypatch.setattr(D, "_run", run)
+    monkeypatch.setattr(D._Structs, "at", structs)
+    return lambda where: [a for entry in made if isinstance(entry, tuple) and entry[0] == where for a in [entry[1]]]
+
+
+def operands(sliced):
+    """Projections read head by head, or slices of one packed projection."""
+    B, N, H, d, dv = 2, 9, 4, 64, 128
+    if sliced:
+        packed = torch.zeros(B, N, H, 4 * d + dv + 8, dtype=BF).transpose(1, 2)
+        views = [packed[..., a:a + w] for a, w in ((0, d), (d, d), (2 * d, d), (3 * d, d), (4 * d + 8, dv))]
+    else:
+        views = [torch.zeros(B, N, H, w, dtype=BF).transpose(1, 2) for w in (d, d, d, d, dv)]
+    return [t.detach().requires_grad_() for t in views] + [torch.zeros(2 * H, dtype=BF)[::2].detach().requires_grad_()]
+
+
+@pytest.mark.parametrize("sliced", [False, True], ids=["token_major", "packed"])
+@pytest.mark.parametrize("unpack", [lambda t: t, lambda t: t.contiguous(), lambda t: t.clone()],
+                         ids=["as_saved", "contiguous", "clone"])
+def test_backward_takes_the_layout_of_what_was_saved(calls, sliced, unpack):
+    """Hooks on saved tensors (offloading, compression) may give back tensors of another layout: addresses
+    and strides that reach the library belong to the same tensors."""
+    ops, back = operands(sliced), []
+
+    def restore(t):
+        t = unpack(t)
+        back.append(t)
+        return t
+
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, restore):
+        O = D.diff_attn(*ops, causal=True)
+    torch.autograd.grad(O, ops, torch.zeros_like(O))
+    (args,) = calls("streamkl_diff_bwd")
+    given = {t.data_ptr(): t for t in back}
+    for place, like in zip(args[2:8], ops):       # Q1, K1, Q2, K2, V, lam
+        assert place.ptr in given
+        t = given[place.ptr]
+        assert t.shape == like.shape
+        want = t.stride()[:-1] if t.dim() == 4 else (0, t.stride(0), 0)
+        assert (place.b, place.h, place.n) == want

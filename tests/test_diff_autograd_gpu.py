@@ -1,0 +1,48 @@
+"""Differential attention and the paged calls in autograd on the GPU."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def operands(layout, seed=7):
+    """Projections read head by head, or slices of one packed projection; lam every second of its elements."""
+    g = torch.Generator().manual_seed(seed)
+    B, N, H, d, dv = 2, 140, 4, 64, 128
+    if layout == "packed":
+        packed = torch.randn(B, N, H, 4 * d + dv + 8, generator=g).to(BF).cuda().transpose(1, 2)
+        views = [packed[..., a:a + w] for a, w in ((0, d), (d, d), (2 * d, d), (3 * d, d), (4 * d + 8, dv))]
+    else:
+        views = [torch.randn(B, N, H, w, generator=g).to(BF).cuda().transpose(1, 2) for w in (d, d, d, d, dv)]
+    lam = torch.rand(2 * H, generator=g).to(BF).cuda()[::2]
+    dO = torch.randn(B, H, N, dv, generator=g).to(BF).cuda()
+    return [t.detach().requires_grad_() for t in (*views, lam)], dO
+
+
+def offload(pin):
+    return torch.autograd.graph.save_on_cpu(pin_memory=pin)
+
+
+def relayout():
+    return torch.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: t.contiguous())
+
+
+@pytest.mark.parametrize("layout", ["token_major", "packed"])
+@pytest.mark.parametrize("hooks", [relayout, lambda: offload(False), lambda: offload(True)],
+                         ids=["contiguous", "save_on_cpu", "save_on_cpu_pinned"])
+def test_saved_tensors_in_another_layout(layout, hooks):
+    """Hooks that give the saved tensors back in another layout leave the gradients as they are, bit for bit."""
+    import attention_kl_distillation_b200 as skl
+    ops, dO = operands(layout)
+    n = torch.tensor([140, 77], dtype=torch.int32, device="cuda")
+    step = lambda: skl.diff_attn(*ops, causal=True, s1=0.2, q_lens=n, k_lens=n)  # noqa: E731
+    want = torch.autograd.grad(step(), ops, dO)
+    with hooks():
+        O = step()
+    got = torch.autograd.grad(O, ops, dO)
+    torch.cuda.synchronize()
+    assert skl.query_device_status() == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
