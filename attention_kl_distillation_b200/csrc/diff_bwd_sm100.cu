@@ -828,8 +828,10 @@ __global__ void __launch_bounds__(256, 4) streamkl_diff_prep_kernel(const DiffPr
   float n1 = -INFINITY, n2 = -INFINITY, lam = 0.f;
   if (threadIdx.x < CB && sees(i0 + threadIdx.x)) {
     const long long v = static_cast<long long>(bh) * p.s.NQ + i0 + threadIdx.x;
-    n1 = -p.LSE1[v] * kLog2e;
-    n2 = -p.LSE2[v] * kLog2e;
+    // LSE = -inf: all visible scores are, and the map has no weights (as in the forward)
+    const float l1 = p.LSE1[v], l2 = p.LSE2[v];
+    n1 = l1 == -INFINITY ? l1 : -l1 * kLog2e;
+    n2 = l2 == -INFINITY ? l2 : -l2 * kLog2e;
     lam = load_lam(p.lam, b, h, i0 + threadIdx.x, F16);
   }
   const int sub = threadIdx.x % L, r0 = threadIdx.x / L;

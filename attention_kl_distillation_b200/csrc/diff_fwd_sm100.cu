@@ -262,12 +262,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       if (!ok) break;
       // Epilogue: the maps exchange 1/l_t, then each warpgroup forms half the columns.
-      const bool seen = l > 0.f;
+      // A row counts by its mask, so that NaN and infinities of what it sees come out.
+      const bool sees = lim > 0;
       if (w.half == 0 && i < p.s.NQ) {
         float* L = t ? p.LSE2 : p.LSE1;
         if (L)
           L[(static_cast<long long>(w.b) * p.s.H + w.h) * p.s.NQ + i] =
-              seen ? kLn2 * (m + lg2(l)) : -INFINITY;
+              sees ? kLn2 * (m + lg2(l)) : -INFINITY;
       }
       // Rows are stored NP lanes together (see transpose_pieces): this lane has one
       // 16-byte piece of each of the NP rows from g0 on.
@@ -291,7 +292,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       oph ^= 1;
       // The value products behind ofull waited until every warp had left the
       // epilogue before, so no one still reads the old 1/l.
-      inv_s[t * R + row] = seen ? 1.f / l : 0.f;
+      // A map whose visible scores are all -inf has no weights (l = 0) and gives 0.
+      inv_s[t * R + row] = l != 0.f ? 1.f / l : 0.f;
       __syncwarp();
       if (lane == 0) mbar_arrive(ifull);
       if (!(ok = mbar_wait(ifull, iph, ctl))) break;
@@ -313,7 +315,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(oempty);  // the next unit's value products may begin
       // rows without a visible key are 0 whatever the accumulators hold
-      const bool live = i1 != 0.f && row_ok;
       const float2 I1 = make_float2(i1, i1), I2 = make_float2(i2, i2), NL = make_float2(-lam, -lam);
       auto pair = [](const uint32_t* v) { return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])); };
       auto pieces = [&](auto second, void* out) {
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // both maps' outputs are rounded alike, so that equal maps cancel exactly
             float2 r = __fmul2_rn(pair(&b[8 * e + 2 * k]), I2);
             if (!decltype(second)::value) r = __ffma2_rn(r, NL, __fmul2_rn(pair(&a[8 * e + 2 * k]), I1));
-            v[k] = live ? pack2<F16>(r.x, r.y) : 0u;
+            v[k] = sees ? pack2<F16>(r.x, r.y) : 0u;
           }
           x[e] = make_uint4(v[0], v[1], v[2], v[3]);
         }

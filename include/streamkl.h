@@ -288,7 +288,9 @@ uint64_t streamkl_launch_count(void);
  * i < q_lens[b], j < k_lens[b] and, if causal, j <= i + k_lens[b] - q_lens[b].
  * Rows that see no key give O = 0, LSE = -inf and no gradient; rows of K, V,
  * Q and dO outside the lengths may hold anything, NaN included, and their
- * gradients are 0.
+ * gradients are 0.  NaN and infinities in what a row sees come out as the
+ * formulas give them; only a map whose visible scores are all -infinity counts
+ * as having no weights (O_t = 0, LSE_t = -inf).
  */
 typedef struct {
   const void *ptr;
