@@ -22,6 +22,7 @@ import functools
 from collections import namedtuple
 
 import torch
+from torch.autograd import forward_ad
 
 from .binding import EINVAL, OK, StreamKLError, _lib, _vp
 
@@ -442,6 +443,18 @@ def _backward(plan, dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_len
     return tuple(outs)
 
 
+def _dual() -> bool:
+    """Whether a level of forward-mode differentiation is open: -1 is the level outside."""
+    return getattr(forward_ad, "_current_level", 0) >= 0
+
+
+def _tracked(*operands):
+    """Whether autograd looks at a call: a gradient is wanted, or an operand has a tangent."""
+    if torch.is_grad_enabled() and any([t is not None and t.requires_grad for t in operands]):
+        return True
+    return _dual() and any([t is not None and forward_ad.unpack_dual(t).tangent is not None for t in operands])
+
+
 class _DiffAttnFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, Q1, K1, Q2, K2, V, lam, q_lens, k_lens):
@@ -470,11 +483,10 @@ def diff_attn(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens=Non
     """Differential attention O [B, H, NQ, dv] with autograd for Q1, K1, Q2, K2, V and lam.
 
     Arguments as in ``diff_attn_fwd``.  O's axes are in Q1's memory order.  Where no gradient is
-    wanted, nothing is saved."""
+    wanted, nothing is saved.  Gradients of gradients and forward-mode tangents are refused."""
     lam = _lam(lam)
     plan = _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2)
-    if torch.is_grad_enabled() and (Q1.requires_grad or K1.requires_grad or Q2.requires_grad or
-                                    K2.requires_grad or V.requires_grad or lam.requires_grad):
+    if _tracked(Q1, K1, Q2, K2, V, lam):
         return _DiffAttnFunction.apply(plan, Q1, K1, Q2, K2, V, lam, q_lens, k_lens)
     return _forward(plan, Q1, K1, Q2, K2, V, lam, q_lens, k_lens, False, None)[0]
 
@@ -532,9 +544,34 @@ class _PagedPlan:
 _paged_plan = _planned(_PagedPlan)
 
 
+class _PagedFunction(torch.autograd.Function):
+    """The paged forms in autograd: their outputs want a gradient where an operand does, and refuse to give
+    one, rather than that it is lost without a word."""
+
+    @staticmethod
+    def forward(ctx, call, out, *operands):
+        O = call()
+        # the caller's buffer stays outside the graph: what is returned shares its memory
+        return O.new_empty(0).set_(O) if O is out[0] else O
+
+    @staticmethod
+    def backward(ctx, dO):
+        raise NotImplementedError("attention over paged caches has no backward: call diff_attn where gradients "
+                                  "are wanted, or detach its operands")
+
+
 def _paged(Q1, K1, Q2, K2, V, lam, table, lens, s1, s2, workspace, out):
     lam = _lam(lam)
-    plan = _paged_plan(*_keys(Q1, K1, Q2, K2, V, lam, table, lens, out), _scale(s1), _scale(s2))
+    operands = (Q1, K1, Q2, K2, V, lam)
+    plan_keys = _keys(*operands, table, lens, out)
+    if _tracked(*operands):
+        return _PagedFunction.apply(
+            lambda: _paged_forward(plan_keys, *operands, table, lens, s1, s2, workspace, out), [out], *operands)
+    return _paged_forward(plan_keys, *operands, table, lens, s1, s2, workspace, out)
+
+
+def _paged_forward(plan_keys, Q1, K1, Q2, K2, V, lam, table, lens, s1, s2, workspace, out):
+    plan = _paged_plan(*plan_keys, _scale(s1), _scale(s2))
     if out is None:
         out = Q1.new_empty(plan.out)
     if plan.empty or plan.no_keys:
@@ -557,7 +594,9 @@ def attn_paged(Q, K, V, table, lens, s=None, workspace=None, out=None):
     not followed and, like a length past the table, recorded for ``query_device_status``.
     The work is split over the device by lens as they are when the kernel runs, so a captured call
     follows lengths that grow.  Results repeat bit for bit.  ``workspace`` may pass a device buffer
-    of at least ``paged_workspace_size`` bytes, 256-byte aligned."""
+    of at least ``paged_workspace_size`` bytes, 256-byte aligned.
+    At most 2048 sequences a call.  There is no backward: where an operand wants a gradient the
+    output does too, and asking for it raises NotImplementedError."""
     return _paged(Q, K, None, None, V, None, table, lens, s, None, workspace, out)
 
 
@@ -622,7 +661,9 @@ def paged_write(rows, caches, slots):
     ``rows`` and ``caches`` are tuples of up to four: rows[k] [T, HK, width] goes into caches[k]
     [pages, page_size, HK, width], row t into slot slots[t] = page * page_size + row of the page
     (int32 or int64 [T]).  A negative slot is skipped, one past the cache is skipped and recorded for
-    ``query_device_status``.  Slots must be distinct; the rest of the caches stays as it was."""
+    ``query_device_status``.  Slots must be distinct, and rows that are views of
+    the caches apart from the slots written; the rest of the caches stays as it was.  No gradient
+    passes through the caches."""
     n = len(rows)
     if not 1 <= n <= 4 or n != len(caches):
         raise ValueError("rows and caches must be tuples of the same length, one to four")

@@ -68,3 +68,54 @@ def test_backward_takes_the_layout_of_what_was_saved(calls, sliced, unpack):
         assert t.shape == like.shape
         want = t.stride()[:-1] if t.dim() == 4 else (0, t.stride(0), 0)
         assert (place.b, place.h, place.n) == want
+
+
+def test_forward_mode_is_refused(calls):
+    """A tangent is not dropped: the call raises, as streamkl's does."""
+    ops = [t.detach() for t in operands(False)]
+    for k in range(6):
+        with torch.autograd.forward_ad.dual_level():
+            dual = [torch.autograd.forward_ad.make_dual(t, torch.ones_like(t)) if j == k else t for j, t in enumerate(ops)]
+            with pytest.raises(NotImplementedError):
+                D.diff_attn(*dual)
+            with torch.no_grad(), pytest.raises(NotImplementedError):
+                D.diff_attn(*dual)
+            assert not D.diff_attn(*ops).requires_grad      # no operand has a tangent
+    assert len(calls("streamkl_diff_fwd")) > 0
+
+
+def paged():
+    z = lambda *s: torch.zeros(*s, dtype=BF)  # noqa: E731
+    return dict(Q1=z(3, 4, 64), K1=z(0, 16, 2, 64), Q2=z(3, 4, 64), K2=z(0, 16, 2, 64), V=z(0, 16, 2, 128),
+                lam=z(4), table=torch.zeros(3, 2, dtype=torch.int32), lens=torch.zeros(3, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("name", ["Q1", "K1", "Q2", "K2", "V", "lam"])
+@pytest.mark.parametrize("own", [False, True], ids=["new", "out"])
+def test_paged_forms_refuse_gradients(calls, name, own):
+    """Where an operand wants a gradient the output does too, and asking for it raises. (Caches without pages:
+    nothing is launched.)"""
+    c = paged()
+    c[name].requires_grad_()
+    out = torch.ones(3, 4, 128, dtype=BF) if own else None
+    one = lambda **k: D.attn_paged(c["Q1"], c["K1"], c["V"], c["table"], c["lens"], **k)  # noqa: E731
+    for call in (lambda **k: D.diff_attn_paged(**c, **k), one):
+        if call is one and name in ("Q2", "K2", "lam"):
+            continue
+        for _ in range(2):      # a buffer is used again and again
+            O = call(out=out)
+            assert O.requires_grad and bool((O == 0).all())
+            if own:
+                assert O.data_ptr() == out.data_ptr() and not out.requires_grad
+            with pytest.raises(NotImplementedError):
+                O.sum().backward()
+        with torch.no_grad():
+            O = call(out=out)
+            assert not O.requires_grad and (out is None or O is out)
+        with torch.autograd.forward_ad.dual_level():
+            d = {**c, name: torch.autograd.forward_ad.make_dual(c[name].detach(), torch.ones_like(c[name]))}
+            with pytest.raises(NotImplementedError):
+                D.diff_attn_paged(**d)
+    c[name].requires_grad_(False)
+    O = D.diff_attn_paged(**c, out=out)
+    assert not O.requires_grad and (out is None or O is out)

@@ -46,3 +46,28 @@ def test_saved_tensors_in_another_layout(layout, hooks):
     assert skl.query_device_status() == 0
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("maps", [1, 2])
+def test_paged_forms_in_a_graph(maps):
+    """A query that wants a gradient changes nothing of the output; asking for the gradient raises."""
+    import attention_kl_distillation_b200 as skl
+    g = torch.Generator().manual_seed(3)
+    t = lambda *s: torch.randn(*s, generator=g).to(BF).cuda()  # noqa: E731
+    Q1, Q2, K1, K2, V, lam = t(2, 4, 64), t(2, 4, 64), t(8, 16, 2, 64), t(8, 16, 2, 64), t(8, 16, 2, 128), t(4)
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    lens = torch.tensor([64, 33], dtype=torch.int32, device="cuda")
+
+    def call(out=None):
+        if maps == 1:
+            return skl.attn_paged(Q1, K1, V, table, lens, out=out)
+        return skl.diff_attn_paged(Q1, K1, Q2, K2, V, lam, table, lens, out=out)
+
+    want, out = call(), torch.empty(2, 4, 128, dtype=BF, device="cuda")
+    Q1.requires_grad_()
+    for buffer in (None, out):
+        O = call(buffer)
+        assert torch.equal(O, want) and O.requires_grad
+        with pytest.raises(NotImplementedError):
+            O.sum().backward()
+    assert torch.equal(out, want) and not out.requires_grad
