@@ -27,9 +27,9 @@
 // P is rounded to 16 bits for the product, as any 16-bit tensor-core product
 // needs; l_t sums the unrounded values.
 //
-// O_t is rescaled only when a row's reference grows by more than 8 (in log2):
-// p then stays below 2^8, inside both 16-bit types, and most tiles skip the
-// round trip of O through registers.
+// O_t is rescaled only when a row's largest score has risen by more than the
+// slack of its type (see WeightRef): p then stays inside the type, and most tiles
+// skip the round trip of O through registers.
 #include "diff_sm100.cuh"
 
 #include <type_traits>
@@ -41,7 +41,6 @@ constexpr int R = kDiffRows;
 constexpr int BK = 128;
 constexpr int NTHREADS = 12 * 32;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;
 constexpr uint32_t kColO = 256;
 
 template <int D>
@@ -113,6 +112,7 @@ template <int D, int DVH, bool F16>
 __global__ void __launch_bounds__(NTHREADS, 1)
     streamkl_diff_fwd_kernel(const __grid_constant__ DiffFwdParams p) {
   using Lay = FwdLay<D>;
+  using Ref = WeightRef<F16>;
   constexpr int NS = Lay::NS;
   // d = 64: the first 64 keys' value products start while the others' weights are
   // formed (B1 H16 N8192 d64/128: 767 against 850 us).  At d = 128 the issuer has
@@ -222,16 +222,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int j = 0; j < BK; j += 2)
           mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-        const float mn = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+        const float most = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        const float top = Ref::top(most, c);
         if (kt == 0) {
-          m = mn;  // no output yet: the value product overwrites O_t
+          m = Ref::at(top);  // no output yet: the value product overwrites O_t
         } else {
-          const bool grow = mn > m + kSlack;
+          const bool grow = top > Ref::limit(m);
           if (__any_sync(0xffffffffu, grow)) {
             // sfull was committed behind PV_t of the tile before, so O_t is complete
-            const float f = grow ? ex2(m - mn) : 1.f;
+            const float to = grow ? Ref::at(top) : m;
+            const float f = grow ? ex2(m - to) : 1.f;
             l *= f;
-            m = grow ? mn : m;
+            m = to;
             rescale<DVH>(ocol, f);
           }
         }

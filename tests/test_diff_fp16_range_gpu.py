@@ -1,0 +1,72 @@
+"""fp16 holds weights far below a row's largest, and gradients of diffuse rows: differential attention and the
+paged forms in fp16 against the definition in 64 bits, with bounds that allow less than half a step of fp16's
+smallest number per weight.
+
+Bounds (u = 2^-11, half a step of fp16; c = Reference's bound of a weight's relative error in fp32 and of the
+hardware exponential): a weight relative to the row's sum is off by u + c of itself (paged: u^2 + c, its rounding's
+remainder goes in too) or by 2^-36: weights are kept relative to a reference that puts the row's largest at 2^11 or
+above, where half of fp16's smallest step, 2^-25, is 2^-36 of it and the row's sum is no less than that largest
+weight. Outputs are rounded once more: u of the value, or 2^-25.
+"""
+import math
+
+import pytest
+import torch
+
+from diff_ref import FLUSH, Reference, group_sum, within
+
+pytestmark = pytest.mark.gpu
+
+HF = torch.float16
+WIDTHS = [(64, 64), (64, 128), (128, 128), (128, 256)]
+
+
+def sink(N, H, HK, d, dv, gaps, at, seed=0):
+    """One token's queries [H, d], keys [HK, N, d] and values of two maps: key `at` scores gaps[t] nats above
+    the others and has the value 0, so that the outputs are what the others' small weights make them."""
+    g = torch.Generator().manual_seed(seed)
+    s = 1 / math.sqrt(d)
+    Q, K = [], []
+    for gap in gaps:
+        q, k = torch.randn(H, d, generator=g) * 0.3, torch.randn(HK, N, d, generator=g)
+        q[:, 0], k[:, :, 0], k[:, at] = 16.0, 0.0, 0.0
+        k[:, at, 0] = gap / 16.0 / s
+        Q.append(q.to(HF).cuda())
+        K.append(k.to(HF).cuda())
+    V = (1 + 0.25 * torch.randn(HK, N, dv, generator=g)) * 2000
+    V[:, at] = 0.0
+    return Q, K, V.to(HF).cuda()
+
+
+def bound(r, factors):
+    low = (2.0 ** -36 + FLUSH) * (r.seen.double() @ r.V.abs())
+    e = [(r.u ** factors + r.c) * (P @ r.V.abs()) + low for P in r.P]
+    return (e[0] + r.lam.abs() * e[1]) * (1 + r.u) + r.u * r.O.abs() + 2.0 ** -25
+
+
+@pytest.mark.parametrize("d,dv", WIDTHS)
+@pytest.mark.parametrize("gaps", [(12.0, 14.0), (16.0, 13.0), (18.0, 17.0), (20.0, 3.0)])
+@pytest.mark.parametrize("at", [0, 130, 2998])
+def test_forward_weights_far_below_the_largest(at, gaps, d, dv):
+    import attention_kl_distillation_b200 as skl
+    Q, K, V = sink(3000, 4, 2, d, dv, gaps, at)
+    rows = 140
+    Q1, Q2 = (q[None, :, None].expand(1, 4, rows, d).contiguous() for q in Q)
+    lam = torch.tensor([0.5, -0.25, 2.0, 0.0], dtype=HF, device="cuda")
+    ops = (Q1, K[0][None], Q2, K[1][None], V[None], lam)
+    r = Reference(*ops)
+    O, _, L1, L2 = skl.diff_attn_fwd(*ops)
+    assert skl.query_device_status() == 0
+    within("O", O, r.O, bound(r, 1))
+    for got, want in ((L1, r.LSE[0]), (L2, r.LSE[1])):
+        within("LSE", got, want, r.tol_LSE)
+
+
+def test_forward_very_large_scores():
+    """Scores of 2^27 and more, whose rounding in 32 bits is many nats: weights stay finite, whichever way they round."""
+    import attention_kl_distillation_b200 as skl
+    g = torch.Generator().manual_seed(1)
+    t = lambda h: (torch.randn(1, h, 1000, 64, generator=g) * 12000).to(HF).cuda()  # noqa: E731
+    ops = (t(4), t(4), t(4), t(4), torch.randn(1, 4, 1000, 64, generator=g).to(HF).cuda(), torch.ones(4, dtype=HF).cuda())
+    for O in skl.diff_attn_fwd(*ops)[:2]:
+        assert bool(torch.isfinite(O).all())
