@@ -38,7 +38,6 @@ constexpr int HB = 8;        // query heads per work item (mma N)
 constexpr int kMaxBatch = 2048;
 constexpr int kJoinThreads = 512;
 constexpr int kBehind = -2147483647 - 1;
-constexpr float kSlack = 8.f;  // a reference grows only by more than this (log2)
 
 template <int D, int DV, int MAPS>
 struct PagedLay {
@@ -355,6 +354,7 @@ template <int D, int DV, int MAPS, bool F16>
 __global__ void __launch_bounds__(NW * 32, 1)
     streamkl_paged_kernel(const __grid_constant__ PagedParams p) {
   using Lay = PagedLay<D, DV, MAPS>;
+  using Ref = WeightRef<F16>;
   constexpr int NST = Lay::NST, WPT = Lay::WPT, MT = Lay::MT;
   constexpr int VP = DV / 8;       // 16-byte pieces of a row
   constexpr int CHUNK = KT * 128;  // bytes of 64 features of a tile
@@ -531,8 +531,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
       for (int m = 0; m < MAPS; ++m)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[m][e] = fmaxf(x[m][e], x[m][e + 2]) * (m ? p.c2 : p.c1);
-          grow = grow || mx[m][e] > st.m[m][e] + kSlack;
+          mx[m][e] = Ref::top(fmaxf(x[m][e], x[m][e + 2]), m ? p.c2 : p.c1);
+          grow = grow || mx[m][e] > Ref::limit(st.m[m][e]);
         }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -542,9 +542,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1)
               mx[m][e] = fmaxf(mx[m][e], __shfl_xor_sync(0xffffffffu, mx[m][e], d));
-            const bool up = mx[m][e] > st.m[m][e] + kSlack;
-            const float f = up ? ex2(st.m[m][e] - mx[m][e]) : 1.f;
-            if (up) st.m[m][e] = mx[m][e];
+            const bool up = mx[m][e] > Ref::limit(st.m[m][e]);
+            const float to = Ref::at(mx[m][e]);
+            const float f = up ? ex2(st.m[m][e] - to) : 1.f;
+            if (up) st.m[m][e] = to;
             st.l[m][e] *= f;
 #pragma unroll
             for (int q = 0; q < MT; ++q) {
@@ -565,9 +566,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
         }
         // P^T as the B operand: heads on rows after the transposition.  P goes in as
         // two 16-bit factors, its rounded value and what the rounding left, so that
-        // the outputs are as exact as fp32 weights would make them; the kernel is
-        // bound by HBM and pays 0 to 2% for the second product (B32 H16 d64/128:
-        // 101 -> 103 us).
+        // the outputs are nearly as exact as fp32 weights would make them: a weight is
+        // off by 2^-16 of itself (bf16), or by 2^-22 of itself or 2^-36 of the row's
+        // largest (fp16, see WeightRef).  The kernel is bound by HBM and pays 0 to 2%
+        // for the second product (B32 H16 d64/128: 101 -> 103 us).
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t w = pack2<F16>(x[m][2 * e], x[m][2 * e + 1]);

@@ -70,3 +70,51 @@ def test_forward_very_large_scores():
     ops = (t(4), t(4), t(4), t(4), torch.randn(1, 4, 1000, 64, generator=g).to(HF).cuda(), torch.ones(4, dtype=HF).cuda())
     for O in skl.diff_attn_fwd(*ops)[:2]:
         assert bool(torch.isfinite(O).all())
+
+
+def paged(K, V, lens, page=32):
+    """Whole sequences' keys and values [HK, N, width] in pages, the same for every sequence."""
+    N = V.shape[1]
+    per = (N + page - 1) // page
+    table = torch.arange(per - 1, -1, -1, dtype=torch.int32, device="cuda").expand(len(lens), per).contiguous()
+
+    def cache(t):
+        c = torch.zeros(per * page, t.shape[0], t.shape[2], dtype=HF, device="cuda")
+        c[:N] = t.transpose(0, 1)
+        return c.view(per, page, *c.shape[1:]).flip(0).contiguous()
+
+    return cache(K[0]), cache(K[1]), cache(V), table, torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("d,dv", WIDTHS)
+@pytest.mark.parametrize("gaps", [(12.0, 14.0), (16.0, 13.0), (18.0, 17.0), (20.0, 3.0)])
+@pytest.mark.parametrize("at", [0, 130, 2998])
+@pytest.mark.parametrize("maps", [1, 2])
+def test_paged_weights_far_below_the_largest(maps, at, gaps, d, dv):
+    import attention_kl_distillation_b200 as skl
+    Q, K, V = sink(3000, 8, 2, d, dv, gaps, at)
+    K1, K2, Vc, table, lens = paged(K, V, [3000, 3000, 2999])
+    Q1, Q2 = (q.expand(3, 8, d).contiguous() for q in Q)
+    lam = torch.linspace(-0.5, 2.0, 8).to(HF).cuda()
+    if maps == 1:
+        got = skl.attn_paged(Q1, K1, Vc, table, lens)
+    else:
+        got = skl.diff_attn_paged(Q1, K1, Q2, K2, Vc, lam, table, lens)
+    assert skl.query_device_status() == 0
+    for b in range(3):      # equal sequences are cut at different tokens: each against the definition
+        n = int(lens[b])
+        r = Reference(Q1[b].view(1, 8, 1, d), K[0][None, :, :n], Q2[b].view(1, 8, 1, d), K[1][None, :, :n], V[None, :, :n],
+                      lam if maps == 2 else torch.zeros((), dtype=HF, device="cuda"))
+        within("O", got[b], r.O[0, :, 0], bound(r, 2)[0, :, 0])
+
+
+@pytest.mark.parametrize("maps", [1, 2])
+def test_paged_very_large_scores(maps):
+    import attention_kl_distillation_b200 as skl
+    g = torch.Generator().manual_seed(1)
+    t = lambda *s: (torch.randn(*s, generator=g) * 12000).to(HF).cuda()  # noqa: E731
+    K1, K2, Vc, table, lens = paged([t(4, 3000, 64) for _ in range(2)], t(4, 3000, 64) / 12000, [3000, 1500])
+    Q1, Q2 = t(2, 4, 64), t(2, 4, 64)
+    got = skl.attn_paged(Q1, K1, Vc, table, lens) if maps == 1 else \
+        skl.diff_attn_paged(Q1, K1, Q2, K2, Vc, torch.ones(4, dtype=HF).cuda(), table, lens)
+    assert bool(torch.isfinite(got).all())
