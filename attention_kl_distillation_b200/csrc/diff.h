@@ -144,6 +144,7 @@ struct DiffBwdParams {
   int nhalf;     // dV-only pass: value columns in groups of 128; SEL 1: maps; 1 or 2
   FastDiv by_heads;  // B * HK (kKV) or B * H (kQ)
   int map0;      // SEL 1: the first map (0 or 1)
+  int lam_rows;  // lam differs among the rows of a head
   // kQ, or null: sums over the keys of P2 G in fp32, a share per compute warpgroup.
   // d2_rows: of every row, [4][B*H][rows padded to 128]; else of the rows of a warp
   // together, [B*H][row tiles][4 warpgroups][4 warps].

@@ -269,7 +269,8 @@ streamkl_status streamkl_diff_bwd(const streamkl_diff_problem* prob, const strea
   };
   p.after_pass = 0;
   p.d2 = nullptr;
-  p.d2_rows = lam->n != 0 || pr.NQ == 1;
+  p.lam_rows = lam->n != 0;
+  p.d2_rows = p.lam_rows || pr.NQ == 1;
   auto run = [&](skl::DiffPass pass, int sel, int nhalf, int map0 = 0) -> streamkl_status {
     p.nhalf = nhalf;
     p.by_heads = skl::FastDiv(static_cast<unsigned>(pr.B) * (pass == skl::kDiffKV ? pr.HK : pr.H));

@@ -161,6 +161,36 @@ __device__ __forceinline__ BwdUnit decode(const DiffBwdParams& p, int u) {
   return w;
 }
 
+// The power of two by which A = P1 - lam P2 of a key unit goes into its product in
+// fp16: the largest that keeps |A| <= 1 + |lam| below 2^15.  A row that spreads over
+// n keys has entries of 1 / n, which no scale of dO changes: without this they
+// would lose bits from n = 2^14 on and vanish at 2^25.  lam of the unit's rows is
+// read from their records by the whole warp: two values a step of the unit, or one
+// a head where a head's rows share it.
+__device__ __forceinline__ float key_scale(const DiffBwdParams& p, const BwdUnit& w, int lane) {
+  float most = 0.f;
+  if (w.tiles > 0) {
+    const float* r = p.rec + static_cast<size_t>(w.b * p.s.H + w.h) * p.NQpad * kDiffRec + 4 * CB;
+    const size_t head = static_cast<size_t>(p.NQpad) * kDiffRec;
+    if (p.lam_rows) {
+      for (int g = 0; g < w.heads; ++g)
+        for (int t = w.c_first; t < w.c_first + w.tiles; ++t) {
+          const float* at = r + g * head + static_cast<size_t>(t) * (CB * kDiffRec) + lane;
+          most = fmaxf(most, fmaxf(fabsf(at[0]), fabsf(at[32])));
+        }
+    } else {
+      const int i = w.hi - 1;  // a row that sees a key, as all of a unit that streams any
+      for (int g = lane; g < w.heads; g += 32)
+        most = fmaxf(most, fabsf(r[g * head + static_cast<size_t>(i / CB) * (CB * kDiffRec) + i % CB]));
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
+  }
+  // 2^e <= 1 + most < 2^(e + 1); the result is 2^(14 - e)
+  const int e = static_cast<int>(__float_as_uint(1.f + most) >> 23) - 127;
+  return __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+}
+
 // X1, X2 and A of one resident row and CPW streamed rows.  Per streamed row
 // (KV) or for the thread's own row: rec = -LSE1 log2e, -LSE2 log2e, D1, D2, lam.
 // Streamed rows i in [lo, hi] are visible (MASK only).
@@ -326,6 +356,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // kQ: X_t = P_t (f_t G + fd_t), f_1 = 1 and f_2 = -lam, fd_t = -f_t D_t
       const float f1 = Lay::ONE && map ? -rec[4] : 1.f, fd1 = -f1 * rec[2];
       const float f2 = -rec[4], fd2 = -f2 * rec[3];
+      const float ascale = Lay::WV && F16 ? key_scale(p, w, lane) : 1.f;
       float2 d2sum = make_float2(0.f, 0.f);
       const int steps = w.heads * w.tiles;
       int tile = 0;
@@ -370,7 +401,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (Lay::WV) {
 #pragma unroll
           for (int i = 0; i < CPW; i += 2) {
-            const float2 x = __ffma2_rn(pair(b, i), NEG, pair(a, i));
+            float2 x = __ffma2_rn(pair(b, i), NEG, pair(a, i));
+            if (F16) x = __fmul2_rn(x, make_float2(ascale, ascale));
             w3[i / 2] = pack2<F16>(x.x, x.y);
           }
         }
@@ -473,7 +505,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const Strides& st = o == 0 ? p.so1 : o == 1 ? p.so2 : p.so3;
         const int cols = (o < 2 ? D : DV) / NWG, first = (o < 2 ? 0 : e.half * DV) + ep * cols;
         const uint32_t col = (Lay::ONE || o == 0 ? Lay::o1 : o == 1 ? Lay::o2 : Lay::o3) + ep * cols;
-        const float f = o == 0 ? p.s1 : o == 1 ? p.s2 : 1.f;
+        const float f = o == 0 ? p.s1 : o == 1 ? p.s2 : 1.f / ascale;
         uint16_t* dst = static_cast<uint16_t*>(base) + e.b * st.b + h * st.h + row * st.n + first;
 #pragma unroll 1
         for (int c = 0; c < cols; c += 16) {

@@ -118,3 +118,62 @@ def test_paged_very_large_scores(maps):
     got = skl.attn_paged(Q1, K1, Vc, table, lens) if maps == 1 else \
         skl.diff_attn_paged(Q1, K1, Q2, K2, Vc, torch.ones(4, dtype=HF).cuda(), table, lens)
     assert bool(torch.isfinite(got).all())
+
+
+def dv_bound(r, dO, lam_max):
+    """dV and its bound, with chains of additions as the kernels have them."""
+    u, eps = r.u, 2.0 ** -23
+    amp = max(float((Q.abs() @ K.abs().transpose(2, 3)).max()) * x for Q, K, x in zip(r.Q, r.K, r.s))
+    c = eps * ((r.d + 4) * amp + r.NK / 128 + 40 + 16)
+    dO = torch.where(r.rows, dO.double(), 0.0)
+    A = r.P[0] - r.lam * r.P[1]
+    e = torch.where(r.seen, u * A.abs() + c * (r.P[0] + r.lam.abs() * r.P[1]) + 2.0 ** -38 * (1 + lam_max)
+                    + FLUSH * (1 + r.lam.abs()), 0.0)
+    v = group_sum(A.transpose(2, 3) @ dO, r.HK)
+    e = group_sum(e.transpose(2, 3) @ dO.abs() + r.NQ * eps * (A.abs().transpose(2, 3) @ dO.abs()), r.HK)
+    return v, e * (1 + u) + u * v.abs() + 2.0 ** -25
+
+
+@pytest.mark.parametrize("d,dv", WIDTHS)
+@pytest.mark.parametrize("NK", [20001, 200001])
+def test_value_gradient_of_diffuse_rows(NK, d, dv):
+    """Rows that spread over very many keys: A is below fp16's normal numbers, the same for a whole row in the
+    first heads (so that its rounding does not average out)."""
+    import attention_kl_distillation_b200 as skl
+    g = torch.Generator(device="cuda").manual_seed(5)
+    t = lambda h, n, w, x: (torch.randn(1, h, n, w, generator=g, device="cuda") * x).to(HF)  # noqa: E731
+    ops = [t(2, 70, d, 0.5), t(1, NK, d, 0.5), t(2, 70, d, 0.5), t(1, NK, d, 0.5), t(1, NK, dv, 1.0),
+           torch.tensor([0.37, -0.21], dtype=HF, device="cuda")]
+    ops[0][:, 0], ops[2][:, 0] = 0.0, 0.0
+    dO = t(2, 70, dv, 1000.0)
+    saved = skl.diff_attn_fwd(*ops)
+    dV = skl.diff_attn_bwd(dO, *ops, *saved, need=(False,) * 4 + (True, False))[4]
+    assert skl.query_device_status() == 0
+    within("dV", dV, *dv_bound(Reference(*ops), dO, 0.37))
+
+
+@pytest.mark.parametrize("d,dv", WIDTHS)
+@pytest.mark.parametrize("weights", ["large", "rows", "late", "zero"])
+def test_value_gradient_of_any_weight(weights, d, dv):
+    """Weights past fp16's range, and weights of very different size in one key head's rows."""
+    import attention_kl_distillation_b200 as skl
+    g = torch.Generator(device="cuda").manual_seed(6)
+    t = lambda h, n, w, x: (torch.randn(2, h, n, w, generator=g, device="cuda") * x).to(HF)  # noqa: E731
+    n = torch.tensor([333, 200], dtype=torch.int32, device="cuda")
+    lam = {"large": torch.tensor([2.0e5, -3.0, 0.5, 1.0e5], device="cuda"), "zero": torch.zeros((), device="cuda"),
+           "rows": torch.randn(2, 4, 333, generator=g, device="cuda") * 0.1,
+           "late": torch.randn(2, 4, 333, generator=g, device="cuda") * 0.1}[weights]
+    if weights == "rows":
+        lam[0, 1, 65], lam[1, 3, 199] = -1000.0, 70.0
+        lam[1, :, 200:] = math.nan                # behind the end
+    if weights == "late":
+        lam[:, 3, -1] = 5.0e4                     # the last row: every key tile's
+    big = float(lam.nan_to_num(0.0).abs().max())
+    ops = [t(4, 333, d, 1.5), t(2, 333, d, 1.0), t(4, 333, d, 1.5), t(2, 333, d, 1.0), t(2, 333, dv, 0.01), lam]
+    dO = t(4, 333, dv, 0.001)
+    kw = dict(causal=True, q_lens=n, k_lens=n)
+    saved = skl.diff_attn_fwd(*ops, **kw)
+    dV = skl.diff_attn_bwd(dO, *ops, *saved, **kw)[4]
+    assert skl.query_device_status() == 0
+    r = Reference(*ops[:5], lam.nan_to_num(0.0), **kw)
+    within("dV", dV, *dv_bound(r, dO, big))
