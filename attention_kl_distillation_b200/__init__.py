@@ -20,9 +20,15 @@ _DIFF_NAMES = ("attn_paged", "diff_attn", "diff_attn_bwd", "diff_attn_fwd", "dif
 __all__ = [*_BINDING_NAMES, *_DIFF_NAMES]
 
 
+_modules = {}  # a public name's module, once it has been asked for
+
+
 def __getattr__(name):
-    module = ".binding" if name in _BINDING_NAMES else ".diff" if name in _DIFF_NAMES else None
+    # The name itself is looked up at every use: what is replaced in a module is replaced here.
+    module = _modules.get(name)
     if module is None:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    value = globals()[name] = getattr(importlib.import_module(module, __name__), name)
-    return value
+        of = ".binding" if name in _BINDING_NAMES else ".diff" if name in _DIFF_NAMES else None
+        if of is None:
+            raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+        module = _modules[name] = importlib.import_module(of, __name__)
+    return getattr(module, name)

@@ -119,3 +119,13 @@ def test_paged_forms_refuse_gradients(calls, name, own):
     c[name].requires_grad_(False)
     O = D.diff_attn_paged(**c, out=out)
     assert not O.requires_grad and (out is None or O is out)
+
+
+def test_public_names_follow_the_binding(monkeypatch):
+    """A function replaced in the binding is the one that the package gives, also after its first use."""
+    import attention_kl_distillation_b200 as skl
+    from attention_kl_distillation_b200 import binding
+    assert skl.fwd is binding.fwd and skl.diff_attn is D.diff_attn
+    monkeypatch.setattr(binding, "fwd", lambda *a: 7)
+    monkeypatch.setattr(D, "diff_attn", lambda *a: 8)
+    assert skl.fwd() == 7 and skl.diff_attn() == 8
