@@ -234,6 +234,13 @@ def _pointers(*tensors):
     return out
 
 
+def _check_places(outs, operands=()):
+    """A caller's outputs start in different places, and not where an operand does."""
+    outs = [p for p in outs if p]
+    if len(set(outs)) != len(outs) or not set(outs).isdisjoint(operands):
+        raise ValueError("outputs must not be in one place with each other or with an operand")
+
+
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
@@ -327,7 +334,8 @@ def diff_attn_fwd(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens
     self-attention batch passes both.  Rows that see no key give O = 0 and LSE = -inf.  Scales of
     None (or <= 0) are 1/sqrt(d).
     O2 = P2 V and the LSEs are what ``diff_attn_bwd`` needs; ``save=False`` leaves them out (None).
-    ``out`` may hold a preallocated O, and with ``save`` O2, LSE1, LSE2."""
+    ``out`` may hold a preallocated O, and with ``save`` O2, LSE1, LSE2, none of them in memory that
+    another output, K1, K2 or V has."""
     lam = _lam(lam)
     plan = _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2)
     return _forward(plan, Q1, K1, Q2, K2, V, lam, q_lens, k_lens, save, out)
@@ -361,6 +369,9 @@ def _forward(plan, Q1, K1, Q2, K2, V, lam, q_lens, k_lens, save, out):
                 t.fill_(v)
         return O, O2, LSE1, LSE2
     p = _pointers(Q1, K1, Q2, K2, V, O, O2)
+    if out is not None:
+        # over Q is well: a block reads its rows of Q before it writes those of O
+        _check_places([*p[5:], *((LSE1.data_ptr(), LSE2.data_ptr()) if save else ())], (p[1], p[3], p[4]))
     block, at = structs.at([*p[:5], lam.data_ptr(), *p[5:]])
     _run(_lib.streamkl_diff_fwd, "streamkl_diff_fwd", plan.device, plan.prob_at, *at[:6], _ptr(q_lens),
          _ptr(k_lens), *at[6:], _ptr(LSE1), _ptr(LSE2))
@@ -392,7 +403,8 @@ def diff_attn_bwd(dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, causal=False, s
     broadcast over.  Accumulation is in fp32 and in a fixed order: results repeat bit for bit.  dS is
     rounded to the inputs' 16-bit type for the products, so an fp32 lam's gradient is as exact as
     16-bit operands allow, and fp16 training wants the usual loss scale.
-    ``out`` may pass preallocated gradients (None entries are skipped), ``workspace`` a device buffer
+    ``out`` may pass preallocated gradients (None entries are skipped), each in memory that no other
+    gradient, dO, Q, K or V has, ``workspace`` a device buffer
     of at least ``diff_attn_workspace_size`` bytes, 256-byte aligned."""
     lam = _lam(lam)
     plan = _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, causal, s1, s2)
@@ -436,6 +448,9 @@ def _backward(plan, dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_len
                 o.zero_()
         return tuple(outs)
     p = _pointers(dO, *inputs, O, O2, *outs[:5])
+    if out is not None:
+        # lam, O and O2 are read by the first kernel alone, before anything is written
+        _check_places([*p[8:], _ptr(outs[5])], p[:6])
     block, at = structs.at([*p[:6], lam.data_ptr(), *p[6:]])
     ws, ws_at, ws_bytes = _workspace(workspace, plan.ws_bytes, Q1)
     _run(_lib.streamkl_diff_bwd, "streamkl_diff_bwd", plan.device, plan.prob_at, *at[:9], _ptr(LSE1),
@@ -670,6 +685,8 @@ def paged_write(rows, caches, slots):
     plan = _write_plan(n, *_keys(*rows, *caches, slots))
     if plan.empty:
         return
-    block, at = plan.structs.at(_pointers(*rows, *caches))
+    p = _pointers(*rows, *caches)
+    _check_places(p[n:])
+    block, at = plan.structs.at(p)
     _run(_lib.streamkl_paged_write, "streamkl_paged_write", plan.device, n, at[0], at[n], plan.widths_at,
          slots.data_ptr(), *plan.tail)

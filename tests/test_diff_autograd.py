@@ -129,3 +129,38 @@ def test_public_names_follow_the_binding(monkeypatch):
     monkeypatch.setattr(binding, "fwd", lambda *a: 7)
     monkeypatch.setattr(D, "diff_attn", lambda *a: 8)
     assert skl.fwd() == 7 and skl.diff_attn() == 8
+
+
+def test_outputs_in_one_place_are_refused(calls):
+    """Two outputs in one place, or an output over an operand that other blocks still read, would be a race."""
+    B, H, N, d = 2, 4, 9, 64
+    z = lambda *s: torch.zeros(*s, dtype=BF)  # noqa: E731
+    ops = [z(B, H, N, d) for _ in range(5)] + [z(H)]
+    O, O2, L1, L2 = z(B, H, N, d), z(B, H, N, d), torch.zeros(B, H, N), torch.zeros(B, H, N)
+    for out in ((O, O, L1, L2), (O, O2, L1, L1), (ops[1], O2, L1, L2), (ops[3], O2, L1, L2), (O, ops[4], L1, L2)):
+        with pytest.raises(ValueError, match="one place"):
+            D.diff_attn_fwd(*ops, out=out)
+    for K in (1, 3, 4):
+        with pytest.raises(ValueError, match="one place"):
+            D.diff_attn_fwd(*ops, save=False, out=(ops[K], None, None, None))
+    dO, grads = z(B, H, N, d), [z(B, H, N, d) for _ in range(5)] + [z(H)]
+    for k in range(5):
+        for other in [*(g for j, g in enumerate(grads[:5]) if j != k), *ops[:5], dO]:
+            out = list(grads)
+            out[k] = other
+            with pytest.raises(ValueError, match="one place"):
+                D.diff_attn_bwd(dO, *ops, O, O2, L1, L2, out=out)
+    assert not calls("streamkl_diff_fwd") and not calls("streamkl_diff_bwd")
+    D.diff_attn_fwd(*ops, out=(O, O2, L1, L2))
+    D.diff_attn_fwd(*ops, out=(ops[0], O2, L1, L2))      # over Q: a block reads its rows before it writes them
+    D.diff_attn_bwd(dO, *ops, O, O2, L1, L2, out=grads)
+    same = ops[:2] + ops[:2] + ops[4:]                   # operands may be the same
+    D.diff_attn_bwd(dO, *same, O, O2, L1, L2, out=grads)
+    D.diff_attn_bwd(dO, *ops, O, O2, L1, L2, out=[O, *grads[1:4], O2, ops[5]])   # read before the passes begin
+    assert len(calls("streamkl_diff_fwd")) == 2 and len(calls("streamkl_diff_bwd")) == 3
+
+    cache, rows, slots = z(3, 16, 2, 64), z(5, 2, 64), torch.zeros(5, dtype=torch.int64)
+    with pytest.raises(ValueError, match="one place"):
+        D.paged_write((rows, rows), (cache, cache), slots)
+    D.paged_write((rows, rows), (cache, z(3, 16, 2, 64)), slots)
+    assert len(calls("streamkl_paged_write")) == 1

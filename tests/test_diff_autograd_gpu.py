@@ -71,3 +71,23 @@ def test_paged_forms_in_a_graph(maps):
         with pytest.raises(NotImplementedError):
             O.sum().backward()
     assert torch.equal(out, want) and not out.requires_grad
+
+
+def test_outputs_over_what_has_been_read():
+    """O over Q1, and gradients over O, O2 and lam, are as in places of their own."""
+    import attention_kl_distillation_b200 as skl
+    g = torch.Generator().manual_seed(9)
+    t = lambda h: torch.randn(2, h, 500, 64, generator=g).to(BF).cuda()  # noqa: E731
+    ops, dO = [t(8), t(8), t(8), t(8), t(8), torch.rand(8, generator=g).to(BF).cuda()], t(8)
+    want = skl.diff_attn_fwd(*ops, causal=True)
+    grads = skl.diff_attn_bwd(dO, *ops, *want, causal=True)
+    O, O2, L1, L2 = (x.clone() for x in want)
+    lam = ops[5].clone()
+    new = [torch.empty_like(x) for x in ops[1:4]]
+    got = skl.diff_attn_bwd(dO, *ops[:5], lam, O, O2, L1, L2, causal=True, out=[O, *new, O2, lam])
+    for a, b in zip(got, grads):
+        assert torch.equal(a, b)
+    over = ops[0].clone()
+    skl.diff_attn_fwd(over, *ops[1:], causal=True, save=False, out=(over, None, None, None))
+    assert torch.equal(over, want[0])
+    assert skl.query_device_status() == 0
