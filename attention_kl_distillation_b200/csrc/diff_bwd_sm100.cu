@@ -194,7 +194,7 @@ __device__ __forceinline__ float key_scale(const DiffBwdParams& p, const BwdUnit
 // X1, X2 and A of one resident row and CPW streamed rows.  Per streamed row
 // (KV) or for the thread's own row: rec = -LSE1 log2e, -LSE2 log2e, D1, D2, lam.
 // Streamed rows i in [lo, hi] are visible (MASK only).
-template <class Lay, bool MASK, bool F16>
+template <class Lay, bool MASK>
 __device__ __forceinline__ void form_p(uint32_t (&s1)[CPW], uint32_t (&s2)[CPW], const float* rr,
                                        const float (&rec)[kDiffRec], float c1, float c2, int lo,
                                        int hi, int map) {
@@ -390,9 +390,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         const float* rr = KV ? rec_s(cs) + part * CPW : nullptr;
         if (masked)
-          form_p<Lay, true, F16>(a, b, rr, rec, map ? p.c2 : p.c1, p.c2, lo, hi, map);
+          form_p<Lay, true>(a, b, rr, rec, map ? p.c2 : p.c1, p.c2, lo, hi, map);
         else
-          form_p<Lay, false, F16>(a, b, rr, rec, map ? p.c2 : p.c1, p.c2, lo, hi, map);
+          form_p<Lay, false>(a, b, rr, rec, map ? p.c2 : p.c1, p.c2, lo, hi, map);
         const float2 NEG = make_float2(-1.f, -1.f);
         uint32_t w1[CPW / 2], w2[CPW / 2], w3[CPW / 2];
         auto pair = [](const uint32_t (&v)[CPW], int i) {
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           mbar_arrive_expect_tx(rfull, Lay::r1 + Lay::r2 + Lay::r3);
           const int rh = KV ? w.hk : w.h;
           const int map = Lay::ONE ? p.map0 + w.half : 0;
-  #pragma unroll
+#pragma unroll
           for (int c = 0; c < D / 64; ++c) {
             if (Lay::S1)
               tma_load_4d(r1_s + c * (R * 128), map ? &p.tmR2 : &p.tmR1, rfull, c * 64, w.r0, rh, w.b);
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           if (Lay::WG) {
             // V is read per key head, dO per query head
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < DV / 64; ++c)
               tma_load_4d(r3_s + c * (R * 128), &p.tmR3, rfull, c * 64, w.r0, rh, w.b);
           }
@@ -570,13 +570,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               const bool ragged = w.ragged(t, nstream);
               uint64_t* bar = ragged ? &craw[cs] : &cfull[cs];
               mbar_arrive_expect_tx(bar, Lay::load_bytes);
-  #pragma unroll
+#pragma unroll
               for (int c = 0; c < D / 64; ++c) {
                 if (Lay::S1)
                   tma_load_4d(c1_s(cs) + c * (CB * 128), map ? &p.tmC2 : &p.tmC1, bar, c * 64, c0, ch, w.b);
                 if (Lay::S2) tma_load_4d(c2_s(cs) + c * (CB * 128), &p.tmC2, bar, c * 64, c0, ch, w.b);
               }
-                auto load3 = [&](int slot, uint64_t* on) {
+              auto load3 = [&](int slot, uint64_t* on) {
 #pragma unroll
                 for (int c = 0; c < DV / 64; ++c)
                   tma_load_4d(c3_s(slot) + c * (CB * 128), &p.tmC3, on, (Lay::ONE ? 0 : w.half) * DV + c * 64, c0, ch,

@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (w.nkt == 0) continue;
           if (!(ok = mbar_wait(qempty, qph ^ 1, ctl))) break;
           mbar_arrive_expect_tx(qfull, 2 * Lay::q_bytes);
-  #pragma unroll
+#pragma unroll
           for (int c = 0; c < D / 64; ++c) {
             tma_load_4d(q1_s + c * (R * 128), &p.tmQ1, qfull, c * 64, w.q0, w.h, w.b);
             tma_load_4d(q2_s + c * (R * 128), &p.tmQ2, qfull, c * 64, w.q0, w.h, w.b);
@@ -388,18 +388,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               step();
             } else {
               if (!(ok = claim(BK * D * 2, false))) break;
-  #pragma unroll
+#pragma unroll
               for (int c = 0; c < D / 64; ++c)
                 tma_load_4d(slot_s(s) + c * (BK * 128), &p.tmK1, bar, c * 64, k0, w.hk, w.b);
               step();
               if (!(ok = claim(BK * D * 2, false))) break;
-  #pragma unroll
+#pragma unroll
               for (int c = 0; c < D / 64; ++c)
                 tma_load_4d(slot_s(s) + c * (BK * 128), &p.tmK2, bar, c * 64, k0, w.hk, w.b);
               step();
             }
             if (!(ok = claim(BK * DVH * 2, w.ragged && kt + 1 == w.nkt))) break;
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < DVH / 64; ++c)
               tma_load_4d(slot_s(s) + c * (BK * 128), &p.tmV, bar, w.half * DVH + c * 64, k0,
                           w.hk, w.b);
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         auto issue_s = [&](int t, uint8_t* tile) {
           const uint64_t kd = sdesc_sw128(smem_u32(tile), 16, 1024);
           const uint64_t qd = here(t ? q2d : q1d);
-  #pragma unroll
+#pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t o = (kk >> 2) * (BK * 128) + (kk & 3) * 32;
             umma_bf16_ss(tmem + t * BK, sdesc_advance(qd, o), sdesc_advance(kd, o), idS, kk > 0);

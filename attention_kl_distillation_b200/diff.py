@@ -216,13 +216,6 @@ def _like_shape(shape, stride, width):
     return [*(shape[k] for k in order), width], back if order != tuple(range(len(order))) else None
 
 
-def _like(m, width):
-    """An empty tensor of m's shape but `width` features, its axes in m's memory order."""
-    shape, back = _like_shape(m.shape, m.stride, width)
-    out = torch.empty(shape, dtype=m.dtype, device=m.device)
-    return out if back is None else out.permute(back)
-
-
 def _pointers(*tensors):
     """Data pointers, 0 for None; operands start on 16 bytes."""
     out = [0 if t is None else t.data_ptr() for t in tensors]
@@ -297,7 +290,7 @@ class _DiffPlan:
         dv = V.shape[3]
         self.keys = [Q1, K1, Q2, K2, V, lam, q_lens, k_lens]
         self.options = causal, s1, s2
-        self.device, self.dtype = Q1.device, Q1.dtype
+        self.device = Q1.device
         self.rows, self.out, self.q = (B, H, NQ), (B, H, NQ, dv), Q1
         self.empty = 0 in self.out or HK == 0
         self.out_shape, self.out_back = _like_shape(Q1.shape, Q1.stride, dv)
@@ -533,7 +526,7 @@ class _PagedPlan:
             raise ValueError("lens must be a contiguous int32 tensor [B] on the inputs' device")
         _check_lens("lens", lens, B, Q1)
         dv = V.shape[3]
-        self.out, self.dtype, self.device = (B, H, dv), Q1.dtype, Q1.device
+        self.out, self.device = (B, H, dv), Q1.device
         if out is not None:
             _check_out("out", out, self.out, Q1)
         _check_cuda(Q1.device)
