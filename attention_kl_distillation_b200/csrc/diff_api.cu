@@ -180,6 +180,10 @@ streamkl_status streamkl_diff_fwd(const streamkl_diff_problem* prob, const strea
   // Once a head has a query tile per SM, the query heads of one key head at a
   // time: the CTAs running together then share its keys and values in L2.
   // Smaller problems interleave all heads, which keeps the last wave short.
+  // Measured, one key head at a time against interleaved: 4096 tokens, H16 d64/128
+  // causal: 186 us against 120; 18944 tokens: 1.98 ms against 2.07; 32768 tokens, H32/8
+  // d128/128 without a mask: 33.0 ms against 35.2.  (Causal at 24576 and more tokens
+  // goes either way: H16/4 d128/128 8.7 ms against 8.4, H16 d64/128 6.8 against 6.9.)
   const int nqt = (pr.NQ + skl::kDiffRows - 1) / skl::kDiffRows;
   p.head_group = nqt >= sms ? pr.H / pr.HK : pr.B * pr.H;
   p.by_group = skl::FastDiv(p.head_group);

@@ -10,8 +10,8 @@
 //             the unrounded P2: as a sum of few large terms it would show the
 //             rounding of O2)
 //
-// Two passes of one kernel template, each with a resident 128-row tile R and
-// streamed 64-row tiles C, so that every gradient is accumulated in TMEM by one
+// Two kinds of pass of one kernel template, each with a resident 128-row tile R
+// and streamed 64-row tiles C, so that every gradient is accumulated in TMEM by one
 // CTA in a fixed order: no atomics, and results that repeat bit for bit.
 //
 //   kDiffKV  R = K1, K2, V   C = Q1, Q2, dO of every query head that shares
@@ -34,18 +34,27 @@
 //
 // TMEM holds 256 output columns beside the 256 above, shared memory the
 // resident tiles and two stages. That decides the passes:
-//   d = 64            kDiffKV gives dK1, dK2 and dV at once
-//   d = 128           dV has a pass of its own (S1, S2 only; 128 value columns)
-//   d = 128, dv = 256 a unit of kDiffKV or kDiffQ has one map (SEL 1, either map):
-//                     V, dO and both maps' tiles do not fit at once
+//   d = 64            two passes: kDiffKV gives dK1, dK2 and dV at once
+//   d = 128           three: dV has a pass of its own (S1, S2 only; 128 value columns)
+//   d = 128, dv = 256 three, with twice the units: one of kDiffKV or kDiffQ has one
+//                     map (SEL 1, either map), as V, dO and both maps' tiles do not
+//                     fit at once, and one of the dV pass a half of the values
 //
 // The passes read the same records and write different outputs, so each starts
 // while the one before still runs (programmatic launch) and takes the
 // multiprocessors as they become free (B1 H16 N4096 d64/128 causal: 347 us against
 // 356).
 //
-// What bounds it: the issue of M128 N64 products, about 64 clocks each whatever
-// their N up to 128, beside 4 exponentials per visible pair over both passes.
+// What bounds it: S and G are M128 N64 products, which hold the tensor pipe for as
+// long as N128 ones.  Over all passes a product is given out every 109 clocks (B1
+// H16 N4096 causal: 353 us at 1845 MHz for d64/128, 593 us at 1762 MHz for
+// d128/128), of which the pipe is busy for 65 to 83.  Beside them every visible
+// pair takes 4 exponentials at d = 64, 6 at d = 128 and 8 at dv = 256.
+//
+// X1, X2 and A are rounded to 16 bits for their products, as any 16-bit tensor-core
+// product needs, after their arithmetic in fp32; D1 and D2 are formed from O and O2
+// as the forward stored them, in 16 bits (dlam, which would show that rounding, is
+// not).  Every sum is in fp32.
 #include "diff_sm100.cuh"
 
 #include <type_traits>

@@ -6,9 +6,10 @@
 // over the first lens[b] tokens of sequence b; token t lives in row t mod
 // page_size of page table[b][t / page_size].
 //
-// What bounds it: every cached row is read once, 2 (maps d + dv) bytes, for
-// 2 g (maps d + dv) FLOP by the g query heads that share it: 8 FLOP a byte at
-// g = 8.  That is HBM, by a factor of 30 under the tensor pipe, so the products
+// What bounds it: every cached row is read once, 2 (maps d + dv) bytes, for the
+// 2 maps g (d + 2 dv) FLOP of the products that the g query heads sharing it issue
+// (a value product per map and factor of the weights): 12 to 20 FLOP a byte at g = 8,
+// where a full tensor pipe would do 250.  That is HBM, so the products
 // use warp-level mma with the keys on M and up to 8 query heads on N (no
 // padding of 8 heads to 128 rows) and each warp streams its own keys through
 // cp.async without a barrier among warps.
