@@ -216,6 +216,19 @@ def _like_shape(shape, stride, width):
     return [*(shape[k] for k in order), width], back if order != tuple(range(len(order))) else None
 
 
+def _low_bits(*tensors):
+    """What the addresses have under 16 bytes."""
+    low = 0
+    for t in tensors:
+        low |= t.data_ptr()
+    return low & 15
+
+
+def _readable(t):
+    """t, or a copy where the kernels cannot read it as it lies."""
+    return t if t.data_ptr() % 16 == 0 and _layout_ok(_meta(t)) else t.clone(memory_format=torch.contiguous_format)
+
+
 def _pointers(*tensors):
     """Data pointers, 0 for None; operands start on 16 bytes."""
     out = [0 if t is None else t.data_ptr() for t in tensors]
@@ -288,7 +301,7 @@ class _DiffPlan:
         lam_strides = _lam_strides(lam, (B, H, NQ), Q1)
         _check_cuda(Q1.device)
         dv = V.shape[3]
-        self.keys = [Q1, K1, Q2, K2, V, lam, q_lens, k_lens]
+        self.saved = None   # the keys of what the forward saves for the backward
         self.options = causal, s1, s2
         self.device = Q1.device
         self.rows, self.out, self.q = (B, H, NQ), (B, H, NQ, dv), Q1
@@ -343,6 +356,8 @@ def _forward(plan, Q1, K1, Q2, K2, V, lam, q_lens, k_lens, save, out):
         structs = plan.fwd.get(save)
         if structs is None:
             structs = plan.fwd[save] = _fwd_structs(plan, _meta(O), _meta(O2))
+            if save:
+                plan.saved = _keys(Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens)
     else:
         out = tuple(out)
         if len(out) != 4:
@@ -475,13 +490,15 @@ class _DiffAttnFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dO):
         need = ctx.needs_input_grad[1:7]
-        if dO.data_ptr() % 16 or not (dO.is_contiguous() or _layout_ok(_meta(dO))):
-            dO = dO.clone(memory_format=torch.contiguous_format)  # expanded or sliced
-        Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens = ctx.saved_tensors
+        dO = _readable(dO)   # expanded or sliced
+        Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens = saved = ctx.saved_tensors
         plan = ctx.plan
         # hooks on saved tensors (offloading, say) may give them back in another layout
-        if _keys(Q1, K1, Q2, K2, V, lam, q_lens, k_lens) != plan.keys:
-            lam = _lam(lam)
+        if _keys(*saved) != plan.saved or _low_bits(Q1, K1, Q2, K2, V, O, O2):
+            Q1, K1, Q2, K2, V, O, O2 = map(_readable, (Q1, K1, Q2, K2, V, O, O2))
+            if O.stride() != O2.stride():
+                O, O2 = O.contiguous(), O2.contiguous()
+            lam, LSE1, LSE2 = _lam(lam), LSE1.contiguous(), LSE2.contiguous()
             plan = _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, *plan.options)
         return (None, *_backward(plan, dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens, need,
                                  None, None), None, None)

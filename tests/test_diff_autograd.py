@@ -70,6 +70,44 @@ def test_backward_takes_the_layout_of_what_was_saved(calls, sliced, unpack):
         assert (place.b, place.h, place.n) == want
 
 
+def off_by_one_element(t):
+    """The same values in memory that starts 2 bytes behind a 16-byte boundary."""
+    flat = torch.empty(t.numel() + 8, dtype=t.dtype)
+    at = flat[1:1 + t.numel()].view(t.shape)
+    return at.copy_(t)
+
+
+def features_apart(t):
+    return t.transpose(-1, -2).contiguous().transpose(-1, -2) if t.dim() == 4 else t
+
+
+def only_small_offsets(t):
+    """A hook that treats some tensors and not others."""
+    only_small_offsets.calls += 1
+    return t.contiguous() if only_small_offsets.calls % 2 else t
+
+
+@pytest.mark.parametrize("unpack", [off_by_one_element, features_apart, only_small_offsets])
+def test_backward_takes_saved_tensors_of_any_layout(calls, unpack):
+    """What the kernels cannot read as it lies is copied, as dO is."""
+    only_small_offsets.calls = 0
+    ops = operands(False)
+    for k, t in enumerate(ops):
+        t.data.copy_(torch.arange(t.numel()).view(t.shape) % 251 + k)
+
+    def restore(t):
+        return unpack(t) if t.dtype == BF else t
+
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, restore):
+        O = D.diff_attn(*ops, causal=True)
+    torch.autograd.grad(O, ops, torch.zeros_like(O))
+    (args,) = calls("streamkl_diff_bwd")
+    for place, like in zip(args[2:7], ops):
+        assert place.ptr % 16 == 0 and all(s % 8 == 0 for s in (place.b, place.h, place.n))
+    O_at, O2_at = args[8], args[9]
+    assert (O_at.b, O_at.h, O_at.n) == (O2_at.b, O2_at.h, O2_at.n)
+
+
 def test_forward_mode_is_refused(calls):
     """A tangent is not dropped: the call raises, as streamkl's does."""
     ops = [t.detach() for t in operands(False)]

@@ -91,3 +91,30 @@ def test_outputs_over_what_has_been_read():
     skl.diff_attn_fwd(over, *ops[1:], causal=True, save=False, out=(over, None, None, None))
     assert torch.equal(over, want[0])
     assert skl.query_device_status() == 0
+
+
+@pytest.mark.parametrize("unpack", ["misaligned", "features_apart", "half_of_them"])
+def test_saved_tensors_of_any_layout(unpack):
+    """Saved tensors that the kernels cannot read as they come back are copied; lam and dO may be anything."""
+    import attention_kl_distillation_b200 as skl
+    ops, dO = operands("token_major", seed=8)
+    seen = [0]
+
+    def restore(t):
+        seen[0] += 1
+        if unpack == "misaligned":
+            flat = torch.empty(t.numel() + 8, dtype=t.dtype, device=t.device)
+            return flat[1:1 + t.numel()].view(t.shape).copy_(t)
+        if unpack == "features_apart":
+            return t.transpose(-1, -2).contiguous().transpose(-1, -2) if t.dim() == 4 else t
+        return t.contiguous() if seen[0] % 2 else t
+
+    want = torch.autograd.grad(skl.diff_attn(*ops, causal=True), ops, dO)
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, restore):
+        O = skl.diff_attn(*ops, causal=True)
+    got = torch.autograd.grad(O, ops, dO, retain_graph=True)
+    again = torch.autograd.grad(O, ops, dO.transpose(2, 3).contiguous().transpose(2, 3))
+    torch.cuda.synchronize()
+    assert skl.query_device_status() == 0
+    for a, b, c in zip(got, again, want):
+        assert torch.equal(a, c) and torch.equal(b, c)
