@@ -420,7 +420,9 @@ def diff_attn_bwd(dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, causal=False, s
                      workspace, out)
 
 
-def _backward(plan, dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens, need, workspace, out):
+def _backward(plan, dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens, need, workspace, out,
+              state=None):
+    """``state``: the keys of O, O2, LSE1 and LSE2 where the caller has them."""
     inputs = (Q1, K1, Q2, K2, V)
     key = structs = None
     if out is not None:
@@ -437,7 +439,7 @@ def _backward(plan, dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_len
     else:
         if len(need) != 6:
             raise ValueError("need must hold six entries: dQ1, dK1, dQ2, dK2, dV, dlam")
-        key = (need, *_keys(dO, O, O2, LSE1, LSE2))
+        key = (need, *_keys(dO), *(state or _keys(O, O2, LSE1, LSE2)))
         structs = plan.bwd.get(key)
         outs = []
         for (shape, back), want in zip(plan.grads, need):
@@ -466,16 +468,17 @@ def _backward(plan, dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_len
     return tuple(outs)
 
 
-def _dual() -> bool:
-    """Whether a level of forward-mode differentiation is open: -1 is the level outside."""
-    return getattr(forward_ad, "_current_level", 0) >= 0
-
-
-def _tracked(*operands):
-    """Whether autograd looks at a call: a gradient is wanted, or an operand has a tangent."""
-    if torch.is_grad_enabled() and any([t is not None and t.requires_grad for t in operands]):
+def _tracked(Q1, K1, Q2, K2, V, lam):
+    """Whether autograd looks at a call (of one map: Q2, K2 and lam are None): a gradient is wanted, or in
+    a level of forward-mode differentiation (-1 is none) an operand has a tangent."""
+    if torch.is_grad_enabled() and (Q1.requires_grad or K1.requires_grad or V.requires_grad or
+                                    (lam is not None and (Q2.requires_grad or K2.requires_grad or
+                                                          lam.requires_grad))):
         return True
-    return _dual() and any([t is not None and forward_ad.unpack_dual(t).tangent is not None for t in operands])
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return False
+    return any(t is not None and forward_ad.unpack_dual(t).tangent is not None
+               for t in (Q1, K1, Q2, K2, V, lam))
 
 
 class _DiffAttnFunction(torch.autograd.Function):
@@ -494,14 +497,17 @@ class _DiffAttnFunction(torch.autograd.Function):
         Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens = saved = ctx.saved_tensors
         plan = ctx.plan
         # hooks on saved tensors (offloading, say) may give them back in another layout
-        if _keys(*saved) != plan.saved or _low_bits(Q1, K1, Q2, K2, V, O, O2):
+        given = _keys(*saved)
+        state = given[6:10]
+        if given != plan.saved or _low_bits(Q1, K1, Q2, K2, V, O, O2):
             Q1, K1, Q2, K2, V, O, O2 = map(_readable, (Q1, K1, Q2, K2, V, O, O2))
             if O.stride() != O2.stride():
                 O, O2 = O.contiguous(), O2.contiguous()
             lam, LSE1, LSE2 = _lam(lam), LSE1.contiguous(), LSE2.contiguous()
             plan = _plan_of(Q1, K1, Q2, K2, V, lam, q_lens, k_lens, *plan.options)
+            state = None
         return (None, *_backward(plan, dO, Q1, K1, Q2, K2, V, lam, O, O2, LSE1, LSE2, q_lens, k_lens, need,
-                                 None, None), None, None)
+                                 None, None, state), None, None)
 
 
 def diff_attn(Q1, K1, Q2, K2, V, lam, causal=False, s1=None, s2=None, q_lens=None, k_lens=None):
@@ -587,16 +593,15 @@ class _PagedFunction(torch.autograd.Function):
 
 def _paged(Q1, K1, Q2, K2, V, lam, table, lens, s1, s2, workspace, out):
     lam = _lam(lam)
-    operands = (Q1, K1, Q2, K2, V, lam)
-    plan_keys = _keys(*operands, table, lens, out)
-    if _tracked(*operands):
+    plan = _paged_plan(*_keys(Q1, K1, Q2, K2, V, lam, table, lens, out), _scale(s1), _scale(s2))
+    if _tracked(Q1, K1, Q2, K2, V, lam):
         return _PagedFunction.apply(
-            lambda: _paged_forward(plan_keys, *operands, table, lens, s1, s2, workspace, out), [out], *operands)
-    return _paged_forward(plan_keys, *operands, table, lens, s1, s2, workspace, out)
+            lambda: _paged_forward(plan, Q1, K1, Q2, K2, V, lam, table, lens, workspace, out), [out],
+            Q1, K1, Q2, K2, V, lam)
+    return _paged_forward(plan, Q1, K1, Q2, K2, V, lam, table, lens, workspace, out)
 
 
-def _paged_forward(plan_keys, Q1, K1, Q2, K2, V, lam, table, lens, s1, s2, workspace, out):
-    plan = _paged_plan(*plan_keys, _scale(s1), _scale(s2))
+def _paged_forward(plan, Q1, K1, Q2, K2, V, lam, table, lens, workspace, out):
     if out is None:
         out = Q1.new_empty(plan.out)
     if plan.empty or plan.no_keys:
