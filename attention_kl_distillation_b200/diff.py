@@ -701,7 +701,8 @@ def paged_write(rows, caches, slots):
     if plan.empty:
         return
     p = _pointers(*rows, *caches)
-    _check_places(p[n:])
+    if len(set(p[n:])) != n:
+        raise ValueError("the caches must not be in one place with each other")
     block, at = plan.structs.at(p)
     _run(_lib.streamkl_paged_write, "streamkl_paged_write", plan.device, n, at[0], at[n], plan.widths_at,
          slots.data_ptr(), *plan.tail)
