@@ -314,6 +314,7 @@ typedef struct {
  * strides broadcast it.  O [B][H][NQ][dv].  O2 (map 2's own output, strides
  * of O2 equal to O's), LSE1 and LSE2 (fp32 [B][H][NQ], contiguous) are the
  * saved state of streamkl_diff_bwd; O2 == NULL, LSE1 == LSE2 == NULL skip them.
+ * Outputs must not overlap each other, K1, K2 or V.
  * Errors: EINVAL (null, unaligned or overlapping layout, sizes out of range,
  * O2 strides other than O's), EUNSUPPORTED (other head widths or dtype, no
  * sm_100 device), ECUDA.
@@ -334,7 +335,8 @@ size_t streamkl_diff_bwd_workspace_size(const streamkl_diff_problem *prob);
  * dQ1, dK1, dQ2, dK2, dV have the shapes of their inputs (any may be NULL); a
  * key head's gradients are summed over the query heads that share it.  dlam,
  * if not NULL, is contiguous in the shape that lam's nonzero strides span
- * ([B or 1][H or 1][NQ or 1]) and of lam's type.  Accumulation is fp32 in a fixed
+ * ([B or 1][H or 1][NQ or 1]) and of lam's type.  Gradients must not overlap each
+ * other, dO, Q1, K1, Q2, K2 or V.  Accumulation is fp32 in a fixed
  * order: results repeat bit for bit.  workspace: as the size above, 256-byte
  * aligned, caller-owned, contents on entry do not matter.
  * Errors: as streamkl_diff_fwd, plus EINVAL for a short or unaligned workspace or no
