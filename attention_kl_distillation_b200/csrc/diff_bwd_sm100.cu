@@ -195,8 +195,9 @@ __device__ __forceinline__ float key_scale(const DiffBwdParams& p, const BwdUnit
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
   }
-  // 2^e <= 1 + most < 2^(e + 1); the result is 2^(14 - e)
-  const int e = static_cast<int>(__float_as_uint(1.f + most) >> 23) - 127;
+  // 2^e <= 1 + most < 2^(e + 1); the result is 2^(14 - e), but no less than 2^-6:
+  // past |lam| = 2^20 entries overflow rather than that other rows' vanish
+  const int e = min(static_cast<int>(__float_as_uint(1.f + most) >> 23) - 127, 20);
   return __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
 }
 

@@ -177,3 +177,21 @@ def test_value_gradient_of_any_weight(weights, d, dv):
     assert skl.query_device_status() == 0
     r = Reference(*ops[:5], lam.nan_to_num(0.0), **kw)
     within("dV", dV, *dv_bound(r, dO, big))
+
+
+def test_a_row_of_infinite_weight_hides_no_other():
+    """One row whose weight overflows: keys that it does not see, in other tiles, keep their gradients."""
+    import attention_kl_distillation_b200 as skl
+    g = torch.Generator(device="cuda").manual_seed(6)
+    t = lambda w, x: (torch.randn(1, 2, 400, w, generator=g, device="cuda") * x).to(HF)  # noqa: E731
+    lam = torch.rand(1, 2, 400, generator=g, device="cuda")
+    lam[0, 0, 100] = 1e30
+    ops, dO = [t(64, 1.0), t(64, 1.0), t(64, 1.0), t(64, 1.0), t(64, 1.0), lam], t(64, 1.0)
+    saved = [x.nan_to_num(0.0, 0.0, 0.0) for x in skl.diff_attn_fwd(*ops, causal=True)]
+    dV = skl.diff_attn_bwd(dO, *ops, *saved, causal=True)[4]
+    assert not bool(torch.isfinite(dV[0, 0, 0]).any())          # key 0 is seen by row 100
+    tame = lam.clone()
+    tame[0, 0, 100] = 0.0                                       # as far as later keys go, the row is not there
+    r = Reference(*ops[:5], tame, True)
+    v, tol = dv_bound(r, dO, 2.0 ** 20)
+    within("dV", dV[:, :, 128:], v[:, :, 128:], tol[:, :, 128:])
